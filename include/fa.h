@@ -339,6 +339,98 @@ int fa_bwd_recompute_range(const void* q, const void* k, const void* v, const vo
                            int kv_end, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Quantised, paged key/value cache, for answering with a trained model: keys
+ * and values of every token so far are kept in 8 bits, and attention of the
+ * newest tokens reads them there.  (The pages describe training; the exact
+ * softmax merge used here over disjoint key sets is section 6.1's split-KV.)
+ *
+ * The caller owns four dense buffers: codes k, v [num_pages][num_kv_heads]
+ * [page_size][d], one byte each, and k_scale, v_scale fp32 [num_pages]
+ * [num_kv_heads][page_size]; all 16-byte aligned.  A row x of d values is
+ *   FA_KV_INT8: scale = amax / 127, code = rint(127 x / amax) (int8)
+ *   FA_KV_FP8:  scale = amax / 448, code = 448 x / amax rounded to e4m3
+ * with amax = max |x|, rounding half to even, and stands for code * scale.  A
+ * row of zeros has scale 0; a row with an infinity or a NaN has a NaN scale, so
+ * every value of it reads as NaN.  page_size is 16, 32, 64 or 128; d is 64 or
+ * 128; num_pages * num_kv_heads * page_size is below 2^31.
+ *
+ * block_table: device int32 [B][max_pages], rows table_stride elements apart:
+ * position p of sequence b is slot p % page_size of page
+ * block_table[b][p / page_size].  Entries past a sequence's last page are not
+ * read.  Page numbers, positions and lengths are read on the device and not
+ * validated on the host: a page outside the cache or a position past the
+ * table is device error 5 (a length out of range: device error 3); it is
+ * never accessed, a written token is dropped, a read one gives zeros, and
+ * attention over it is not meaningful.
+ */
+#define FA_KV_INT8 0
+#define FA_KV_FP8 1
+typedef struct fa_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_pages, page_size, num_kv_heads, d, format;
+} fa_kv_cache;
+
+/*
+ * fa_kv_append quantises k, v (bf16, token-major [total_tokens][num_kv_heads]
+ * [d], strides[2] for k and v: .n token, .h head, multiples of 8 elements)
+ * into the cache.  Sequence b's tokens are rows [cu_seqlens[b],
+ * cu_seqlens[b + 1]) (device int32 [B + 1], non-decreasing; NULL: one token per
+ * sequence, total_tokens = B) and go to positions starts[b], starts[b] + 1, ...
+ * (device int32 [B]; NULL: from 0).  Rows of no sequence are ignored.  Two
+ * tokens must not name the same slot (sequences may share the pages before
+ * their starts, not those they write): which bytes of the two remain is not
+ * defined.
+ * fa_kv_read is the way back: rows of k, v get the values of those positions,
+ * code * scale rounded to bf16.  Rows of no sequence are left as they were.
+ * One launch each.  Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (d),
+ * FA_ERR_ALIGNMENT, FA_ERR_TOO_LARGE, FA_ERR_CUDA; B = 0 or total_tokens = 0 is
+ * an empty problem.
+ */
+int fa_kv_append(const fa_kv_cache* cache, const void* k, const void* v, const fa_strides* strides,
+                 const int32_t* block_table, int max_pages, int64_t table_stride, const int32_t* starts,
+                 const int32_t* cu_seqlens, int B, int total_tokens, void* stream);
+int fa_kv_read(const fa_kv_cache* cache, void* k, void* v, const fa_strides* strides, const int32_t* block_table,
+               int max_pages, int64_t table_stride, const int32_t* starts, const int32_t* cu_seqlens, int B,
+               int total_tokens, void* stream);
+
+/*
+ * Attention of each sequence's newest tokens over its cached keys and values
+ * (which the caller has appended, the newest tokens' own included).  q, o:
+ * bf16, token-major [total_q][Hq][d], strides[2] for q and o; lse: fp32 [Hq]
+ * [total_q] or NULL.  Hq is a multiple of num_kv_heads: query head h reads key
+ * head h / (Hq / num_kv_heads).  Sequence b's queries are rows
+ * [cu_seqlens_q[b], cu_seqlens_q[b + 1]), at most max_q of them (host; NULL:
+ * exactly max_q each, total_q = B * max_q); it has seqlens[b] keys (device int32
+ * [B]).  Of its L queries, query i sees keys j < seqlens[b], and when causal
+ * j < seqlens[b] - L + i + 1: the queries are the sequence's last tokens.  A
+ * query that sees no key gets o = 0 and lse = -inf; rows of no sequence are
+ * left as they were.  The dequantised keys and values enter the products
+ * exactly, the probabilities rounded to f16.  Results do not depend on the
+ * workspace's contents and are the same from run to run.
+ *
+ * prefix_len > 0 (a multiple of page_size, at most max_pages * page_size)
+ * declares that every sequence's first prefix_len keys are the same pages --
+ * those of block_table's first row, the only row read for them: the batch's
+ * queries then attend to them together, each page read once instead of once a
+ * sequence, and the two parts are merged exactly.  The result is that of
+ * prefix_len = 0 up to rounding; a sequence may be shorter than the prefix.
+ *
+ * The work is cut on the device from the lengths, so a captured launch may be
+ * replayed with other lengths, tables and contents.  workspace: 16-byte
+ * aligned, at least fa_fwd_kvcache_workspace_size bytes; calls that may overlap
+ * need one each.  Two launches (three with a prefix).  Errors as fa_kv_append,
+ * and FA_ERR_WORKSPACE.
+ */
+size_t fa_fwd_kvcache_workspace_size(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len);
+int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides, const fa_kv_cache* cache,
+                   const int32_t* block_table, int max_pages, int64_t table_stride, const int32_t* seqlens,
+                   const int32_t* cu_seqlens_q, int B, int Hq, int total_q, int max_q, float scale, int causal,
+                   int prefix_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Debug export of the dropout mask: for each listed head bh = b*H + h
  * (heads[nheads]) and query row (rows[nrows]), writes the keep bit of every
  * key j < N to out[(hi * nrows + ri) * N + j] (1 = kept).  heads, rows and
@@ -402,7 +494,8 @@ int fa_last_cuda_error(void);
  * word.  Returns 0 if no kernel reported an error since the last read, else
  * the kernel's code (1 = a bounded wait timed out, 2 = shared memory
  * misaligned, 3 = variable-length offsets or lengths out of range, 4 = a
- * bounds check failed, bounds-checking build only);
+ * bounds check failed, bounds-checking build only, 5 = a page number outside
+ * the cache or a position past the block table);
  * FA_ERR_CUDA if the synchronisation itself failed.
  */
 int fa_get_device_error(void* stream);

@@ -36,10 +36,14 @@ EXPORTS = ("fa_fwd", "fa_fwd_strided", "fa_fwd_splitkv", "fa_fwd_splitkv_workspa
            "fa_debug_build", "fa_debug_bounds_record",
            "fa_fwd_varlen", "fa_bwd_varlen", "fa_bwd_varlen_workspace_size",
            "fa_fwd_partial", "fa_merge_partials", "fa_weight_partial", "fa_bwd_dq_accumulator_bytes", "fa_bwd_recompute_range",
+           "fa_kv_append", "fa_kv_read", "fa_fwd_kvcache", "fa_fwd_kvcache_workspace_size",
            "fa_dropout_mask", "fa_strerror",
            "fa_last_cuda_error", "fa_get_device_error", "fa_version")
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
+
+# formats of the quantised key/value cache (fa.h: FA_KV_INT8, FA_KV_FP8) by the dtype of its codes
+KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -48,6 +52,13 @@ _lib = None
 class FaStrides(ctypes.Structure):
     """Element strides (batch, head, row) of a [B,H,N,d] tensor, d contiguous."""
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class FaKvCache(ctypes.Structure):
+    """The quantised, paged key/value cache (fa.h: fa_kv_cache)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 class FaError(RuntimeError):
@@ -135,6 +146,12 @@ def _open(path: str) -> ctypes.CDLL:
     lib.fa_bwd_dq_accumulator_bytes.argtypes = [I, I, I, I]
     lib.fa_bwd_dq_accumulator_bytes.restype = SZ
     lib.fa_bwd_recompute_range.argtypes = [vp, vp, vp, vp, vp, vp, I, I, I, I, F, I, F, U64, I, I, vp, SZ, vp]
+    KC, I64 = ctypes.POINTER(FaKvCache), ctypes.c_int64
+    lib.fa_kv_append.argtypes = [KC, vp, vp, SP, vp, I, I64, vp, vp, I, I, vp]
+    lib.fa_kv_read.argtypes = [KC, vp, vp, SP, vp, I, I64, vp, vp, I, I, vp]
+    lib.fa_fwd_kvcache.argtypes = [vp, vp, vp, SP, KC, vp, I, I64, vp, vp, I, I, I, I, F, I, I, vp, SZ, vp]
+    lib.fa_fwd_kvcache_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.fa_fwd_kvcache_workspace_size.restype = SZ
     lib.fa_strerror.argtypes = [I]
     lib.fa_strerror.restype = ctypes.c_char_p
     lib.fa_get_device_error.argtypes = [vp]
@@ -143,7 +160,7 @@ def _open(path: str) -> ctypes.CDLL:
                lib.fa_fwd_blocksparse, lib.fa_bwd_blocksparse, lib.fa_bwd_recompute_blocksparse,
                lib.fa_debug_fwd_timeout, lib.fa_debug_exp2_poly, lib.fa_fwd_varlen, lib.fa_bwd_varlen, lib.fa_fwd_partial,
                lib.fa_merge_partials, lib.fa_weight_partial, lib.fa_bwd_recompute_range,
-               lib.fa_dropout_mask, lib.fa_get_device_error,
+               lib.fa_kv_append, lib.fa_kv_read, lib.fa_fwd_kvcache, lib.fa_dropout_mask, lib.fa_get_device_error,
                lib.fa_last_cuda_error, lib.fa_version, lib.fa_debug_build, lib.fa_debug_bounds_record):
         fn.restype = I
     return lib
@@ -525,6 +542,175 @@ def bwd_finalize(dq, workspace, scale, stream=None):
                                  int(workspace.numel() * workspace.element_size()), _stream(stream)),
           "fa_bwd_finalize")
     return dq
+
+
+def _on(device, stream):
+    """(context, stream handle) for a call on tensors of ``device``: its context makes that device and the given
+    stream current, so that what is allocated inside belongs to them; None needs no context."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return None, torch.cuda.current_stream().cuda_stream
+        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def kv_cache(k, v, k_scale, v_scale) -> FaKvCache:
+    """The C-ABI view of a cache's buffers: codes ``k``, ``v`` [num_pages, num_kv_heads, page_size, d] int8 or
+    float8_e4m3fn and fp32 ``k_scale``, ``v_scale`` [num_pages, num_kv_heads, page_size], dense CUDA tensors.  It holds
+    addresses only; the tensors must outlive it."""
+    for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+        if t.device != k.device:
+            raise ValueError("the cache's tensors must be on one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if k.dtype not in KV_FORMATS or v.dtype != k.dtype:
+        raise ValueError("k and v must both be int8 or both float8_e4m3fn")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("k and v must be [num_pages, num_kv_heads, page_size, d] of one shape")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise ValueError("k_scale and v_scale must be float32")
+    if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+        raise ValueError("k_scale and v_scale must be [num_pages, num_kv_heads, page_size]")
+    P, H, ps, d = k.shape
+    return FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, ps, H, d,
+                     KV_FORMATS[k.dtype])
+
+
+def _check_ints(name, t, device, n=None):
+    """A dense int32 vector (of n entries) on the cache's device."""
+    if t.device != device or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries")
+
+
+def _check_table(block_table, device):
+    """int32 [B, max_pages] on the cache's device, rows dense and apart."""
+    t = block_table
+    if t.device != device or t.dtype != torch.int32 or t.dim() != 2:
+        raise ValueError("block_table must be an int32 [B, max_pages] tensor on the cache's device")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("the rows of block_table must not overlap")
+    return t.shape
+
+
+def _check_tokens(name, t, shape, device):
+    """bf16 [T, H, d] on the cache's device."""
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the cache's device (there is no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _rows_usable(t) -> bool:
+    """Rows the kernels can address directly: unit last stride, 16-byte aligned row starts."""
+    return t.stride(-1) == 1 and t.stride(0) >= 0 and t.stride(1) >= 0 and t.stride(0) % 8 == 0 \
+        and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0
+
+
+def _kv_rows(fn, what, cache, tensors, k, v, block_table, starts, cu_seqlens, stream):
+    device = tensors[0].device
+    B, max_pages = _check_table(block_table, device)
+    T = k.shape[0]
+    if starts is not None:
+        _check_ints("starts", starts, device, B)
+    if cu_seqlens is not None:
+        _check_ints("cu_seqlens", cu_seqlens, device, B + 1)
+    elif T != B:
+        raise ValueError("without cu_seqlens there is one token per sequence")
+    ctx, s = _on(device, stream)
+    with ctx if ctx is not None else contextlib.nullcontext():
+        if fn.__name__ == "fa_kv_append":  # inputs of other layouts are copied once, on the call's stream
+            k, v = (t if _rows_usable(t) else t.contiguous() for t in (k, v))
+        _call(fn(ctypes.byref(cache), _ptr(k), _ptr(v), _tok_strides(k, v), _ptr(block_table), max_pages,
+                 block_table.stride(0), _ptr(starts), _ptr(cu_seqlens), B, T, s), what)
+
+
+def kv_append(cache, tensors, k, v, block_table, starts=None, cu_seqlens=None, stream=None):
+    """Quantise bf16 ``k``, ``v`` [T, num_kv_heads, d] into a cache (``kv_cache`` of ``tensors``, its four buffers) via
+    ``fa_kv_append``."""
+    P, H, ps, d = tensors[0].shape
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, num_kv_heads, d]")
+    _check_tokens("k", k, (k.shape[0], H, d), tensors[0].device)
+    _check_tokens("v", v, (k.shape[0], H, d), tensors[0].device)
+    _kv_rows(load().fa_kv_append, "fa_kv_append", cache, tensors, k, v, block_table, starts, cu_seqlens, stream)
+
+
+def kv_read(cache, tensors, block_table, total_tokens, starts=None, cu_seqlens=None, k=None, v=None, stream=None):
+    """bf16 k, v [total_tokens, num_kv_heads, d] of a cache's positions via ``fa_kv_read``."""
+    P, H, ps, d = tensors[0].shape
+    device = tensors[0].device
+    shape = (int(total_tokens), H, d)
+    ctx, s = _on(device, stream)
+    if k is None or v is None:
+        with ctx if ctx is not None else contextlib.nullcontext():
+            k = torch.empty(shape, dtype=torch.bfloat16, device=device) if k is None else k
+            v = torch.empty(shape, dtype=torch.bfloat16, device=device) if v is None else v
+    _check_tokens("k", k, shape, device)
+    _check_tokens("v", v, shape, device)
+    _kv_rows(load().fa_kv_read, "fa_kv_read", cache, tensors, k, v, block_table, starts, cu_seqlens, stream)
+    return k, v
+
+
+def fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len=0) -> int:
+    return int(load().fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len))
+
+
+def fwd_kvcache(q, cache, tensors, block_table, seqlens, max_q, cu_seqlens_q=None, causal=True, scale=None,
+                prefix_len=0, o=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """O [T, Hq, d] and lse [Hq, T] (or None) of the newest tokens' attention over a cache via ``fa_fwd_kvcache``."""
+    P, Hkv, ps, d = tensors[0].shape
+    device = tensors[0].device
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq, _ = q.shape
+    _check_tokens("q", q, (T, Hq, d), device)
+    if Hq % Hkv != 0:
+        raise ValueError(f"the {Hq} query heads are not a multiple of the cache's {Hkv} heads")
+    B, max_pages = _check_table(block_table, device)
+    _check_ints("seqlens", seqlens, device, B)
+    if cu_seqlens_q is not None:
+        _check_ints("cu_seqlens_q", cu_seqlens_q, device, B + 1)
+    elif B * max_q != T:
+        raise ValueError("without cu_seqlens_q every sequence has max_q queries")
+    if prefix_len % ps != 0 or not 0 <= prefix_len <= max_pages * ps:
+        raise ValueError("prefix_len must be a multiple of the page size within the block table")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load()
+    ctx, s = _on(device, stream)
+    with ctx if ctx is not None else contextlib.nullcontext():
+        if not _rows_usable(q):
+            q = q.contiguous()
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+        else:
+            _check_tokens("o", o, (T, Hq, d), device)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if want_lse else None
+        elif lse.device != device or lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on the cache's device")
+        if workspace is None:
+            need = lib.fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, T, max_q, prefix_len)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        _call(lib.fa_fwd_kvcache(_ptr(q), _ptr(o), _ptr(lse), _tok_strides(q, o), ctypes.byref(cache),
+                                 _ptr(block_table), max_pages, block_table.stride(0), _ptr(seqlens),
+                                 _ptr(cu_seqlens_q), B, Hq, T, max_q, float(scale), int(bool(causal)), prefix_len,
+                                 _ptr(workspace), workspace.numel() * workspace.element_size(), s), "fa_fwd_kvcache")
+    return o, lse
 
 
 def dropout_mask(B, H, N, dropout_p, seed, heads, rows, device="cuda", stream=None):

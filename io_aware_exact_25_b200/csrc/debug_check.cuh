@@ -34,6 +34,12 @@ enum DbgSite : int {
   kSiteBwdKV = 16,       // fused backward: dK, dV row store
   kSiteBwdPost = 17,     // dQ conversion: accumulator read, dQ row store
   kSiteVarlenPad = 20,   // variable-length padding fill
+  kSiteKvRow = 30,       // quantised cache: row (codes and scale) read or written
+  kSiteKvO = 31,         // attention over the cache: O row store
+  kSiteKvLse = 32,       // attention over the cache: lse store
+  kSiteKvPart = 33,      // attention over the cache: piece store
+  kSiteKvRes = 34,       // attention over the cache: result row of a phase
+  kSiteKvQ = 35,         // attention over the cache: Q row read
 };
 
 #ifdef FA_DEBUG

@@ -16,6 +16,7 @@
 #include "bwd_sm100.cuh"
 #include "dropout_hash.cuh"
 #include "fwd_sm100.cuh"
+#include "host.h"
 
 namespace {
 
@@ -41,9 +42,7 @@ int cuda_fail(cudaError_t e) {
 
 // cuTensorMapEncodeTiled, fetched from the driver through the runtime so the
 // library needs no link-time dependency on libcuda.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using fa_host::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
@@ -250,6 +249,12 @@ int check_varlen(int B, int H, int max_seqlen, int total, int d, float scale, in
 }
 
 }  // namespace
+
+namespace fa_host {
+int cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+int* device_error_ptr() { return ::device_error_ptr(); }
+EncodeTiledFn encode_fn() { return ::encode_fn(); }
+}  // namespace fa_host
 
 extern "C" {
 

@@ -1,0 +1,379 @@
+// fa_kvcache.cu -- host side of the quantised key/value cache and of the
+// attention over it (fa_kv_append, fa_kv_read, fa_fwd_kvcache): argument
+// checks, the choice of kernel, tensor maps and launches on the caller's
+// stream.  Allocates nothing and keeps nothing between calls.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "host.h"
+#include "kvcache_sm100.cuh"
+#include "kvnarrow_sm100.cuh"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool tok_strides_ok(const fa_strides& s) {
+  return s.h >= 0 && s.n >= 0 && (s.h * 2) % 16 == 0 && (s.n * 2) % 16 == 0;
+}
+
+size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
+
+int page_shift(int page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    default: return -1;
+  }
+}
+
+// The cache's own checks (sizes first, so that a bad size is refused before a pointer is looked at).
+int check_cache(const fa_kv_cache* c) {
+  if (!c) return FA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_kv_heads < 1) return FA_ERR_INVALID_ARG;
+  if (page_shift(c->page_size) < 0) return FA_ERR_INVALID_ARG;
+  if (c->format != FA_KV_INT8 && c->format != FA_KV_FP8) return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  // rows are addressed by a 32-bit tile coordinate
+  if (c->num_kv_heads > (1 << 16) || (long long)c->num_pages * c->num_kv_heads * c->page_size > 0x7fffffffll)
+    return FA_ERR_TOO_LARGE;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return FA_ERR_ALIGNMENT;
+  return FA_OK;
+}
+
+// Block table and batch: FA_OK, a negative status, or 1 for nothing to do.
+int check_batch(const int32_t* table, int max_pages, int64_t table_stride, int B, int total) {
+  if (B < 0 || total < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || total == 0) return 1;
+  if (B > (1 << 24) || total > (1 << 30)) return FA_ERR_TOO_LARGE;
+  if (max_pages < 1 || !table || (B > 1 && table_stride < max_pages)) return FA_ERR_INVALID_ARG;
+  if (!aligned(table, 4)) return FA_ERR_ALIGNMENT;
+  return FA_OK;
+}
+
+void fill_cache(fa::KvArgs* a, const fa_kv_cache* c) {
+  std::memset(a, 0, sizeof(*a));
+  a->k = static_cast<uint8_t*>(c->k);
+  a->v = static_cast<uint8_t*>(c->v);
+  a->ks = c->k_scale;
+  a->vs = c->v_scale;
+  a->num_pages = c->num_pages;
+  a->page_shift = page_shift(c->page_size);
+  a->Hkv = c->num_kv_heads;
+}
+
+// fa_kv_append and fa_kv_read: everything but the kernel.
+int rows_setup(const fa_kv_cache* c, const void* k, const void* v, const fa_strides* strides, const int32_t* table,
+               int max_pages, int64_t table_stride, const int32_t* starts, const int32_t* cu_seqlens, int B, int total,
+               fa::KvArgs* a) {
+  int rc = check_cache(c);
+  if (rc != FA_OK) return rc;
+  if ((rc = check_batch(table, max_pages, table_stride, B, total)) != FA_OK) return rc;
+  if (!cu_seqlens && total != B) return FA_ERR_INVALID_ARG;
+  if (!k || !v || !strides) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(cu_seqlens, 4)) return FA_ERR_ALIGNMENT;
+  if (!tok_strides_ok(strides[0]) || !tok_strides_ok(strides[1])) return FA_ERR_ALIGNMENT;
+  fill_cache(a, c);
+  a->table = table;
+  a->max_pages = max_pages;
+  a->table_stride = table_stride;
+  a->lens = starts;
+  a->cu = cu_seqlens;
+  a->B = B;
+  a->total = total;
+  a->xk = static_cast<__nv_bfloat16*>(const_cast<void*>(k));
+  a->xv = static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+  a->xk_sn = strides[0].n;
+  a->xk_sh = strides[0].h;
+  a->xv_sn = strides[1].n;
+  a->xv_sh = strides[1].h;
+  a->err = fa_host::device_error_ptr();
+  return a->err ? FA_OK : fa_host::cuda_fail(cudaErrorInvalidSymbol);
+}
+
+template <int D>
+int launch_rows(const fa::KvArgs& a, int format, bool append, cudaStream_t st) {
+  const long long units = (2ll * a.Hkv + fa::kv_rows_per_unit<D>() - 1) / fa::kv_rows_per_unit<D>() * a.total;
+  const long long blocks = (units + 7) / 8;
+  if (blocks > 0x7fffffffll) return FA_ERR_TOO_LARGE;
+  const unsigned grid = (unsigned)blocks;
+  if (append) {
+    if (format == FA_KV_INT8) fa::kv_append_kernel<D, fa::kKvInt8><<<grid, 256, 0, st>>>(a);
+    else fa::kv_append_kernel<D, fa::kKvFp8><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (format == FA_KV_INT8) fa::kv_read_kernel<D, fa::kKvInt8><<<grid, 256, 0, st>>>(a);
+    else fa::kv_read_kernel<D, fa::kKvFp8><<<grid, 256, 0, st>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+}
+
+// Tensor map of the cache's codes as [rows, d] bytes, read in box_rows-row boxes swizzled by the row's width.
+int make_code_map(CUtensorMap* m, const void* base, const fa_kv_cache* c, int box_rows) {
+  fa_host::EncodeTiledFn enc = fa_host::encode_fn();
+  if (!enc) return fa_host::cuda_fail(cudaErrorNotSupported);
+  cuuint64_t dims[2] = {(cuuint64_t)c->d, (cuuint64_t)c->num_pages * c->num_kv_heads * c->page_size};
+  cuuint64_t strides[1] = {(cuuint64_t)c->d};
+  cuuint32_t box[2] = {(cuuint32_t)c->d, (cuuint32_t)box_rows};
+  cuuint32_t estride[2] = {1u, 1u};
+  const CUresult r =
+      enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estride,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : fa_host::cuda_fail(cudaErrorInvalidValue);
+}
+
+// ------------------------------------------------------------- attention
+
+constexpr int kSms = 148;
+
+template <int D, int MT>
+struct NarrowOf;
+template <>
+struct NarrowOf<128, 1> { using L = fa::KvNarrowLayout<128, 1, 3, 2>; };
+template <>
+struct NarrowOf<128, 2> { using L = fa::KvNarrowLayout<128, 2, 3, 2>; };
+template <>
+struct NarrowOf<64, 1> { using L = fa::KvNarrowLayout<64, 1, 4, 3>; };
+template <>
+struct NarrowOf<64, 2> { using L = fa::KvNarrowLayout<64, 2, 4, 2>; };
+
+// The kernel for items of `rows` rows: rows per item tile and stretches the work is cut into.
+struct Choice {
+  int M, G;
+};
+
+Choice choose(long long rows, int d) {
+  if (rows <= 16) return {16, kSms * (d == 128 ? NarrowOf<128, 1>::L::kCtasPerSm : NarrowOf<64, 1>::L::kCtasPerSm)};
+  return {32, kSms * (d == 128 ? NarrowOf<128, 2>::L::kCtasPerSm : NarrowOf<64, 2>::L::kCtasPerSm)};
+}
+
+struct Pieces {
+  size_t o, lse, end;  // byte offsets in the workspace
+};
+
+Pieces place_pieces(size_t at, const Choice& c, int d) {
+  Pieces p;
+  const size_t rows = 2ull * c.G * c.M;
+  p.o = at;
+  p.lse = p.o + rows * d * 4;
+  p.end = round_up(p.lse + rows * 4, 256);
+  return p;
+}
+
+// Workspace: the pieces of one launch, or, with a shared prefix, the pieces and result rows of both phases and the
+// sequences' places on the suffix's line of work.
+struct Layout {
+  Choice whole, prefix, suffix;
+  Pieces pw, pp, ps;
+  size_t prefix_o, prefix_lse, suffix_o, suffix_lse, off, bytes;
+};
+
+Layout layout_of(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len) {
+  Layout l;
+  std::memset(&l, 0, sizeof(l));
+  const int g = Hq / Hkv;
+  if (prefix_len == 0) {
+    l.whole = choose((long long)max_q * g, d);
+    l.pw = place_pieces(0, l.whole, d);
+    l.bytes = l.pw.end;
+    return l;
+  }
+  l.prefix = choose((long long)total_q * g, d);
+  l.suffix = choose((long long)max_q * g, d);
+  l.pp = place_pieces(0, l.prefix, d);
+  l.ps = place_pieces(l.pp.end, l.suffix, d);
+  const size_t rows = (size_t)total_q * Hq;
+  l.prefix_o = l.ps.end;
+  l.suffix_o = l.prefix_o + rows * d * 4;
+  l.prefix_lse = l.suffix_o + rows * d * 4;
+  l.suffix_lse = l.prefix_lse + rows * 4;
+  l.off = round_up(l.suffix_lse + rows * 4, 256);
+  l.bytes = l.off + ((size_t)B + 1) * 8;
+  return l;
+}
+
+template <int D, int FMT, int MT>
+int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  using L = typename NarrowOf<D, MT>::L;
+  auto kern = fa::kv_narrow_kernel<D, FMT, MT, L>;
+  CUtensorMap mk, mv;
+  const int box = c->page_size < 32 ? c->page_size : 32;
+  int rc;
+  if ((rc = make_code_map(&mk, c->k, c, box)) != FA_OK) return rc;
+  if ((rc = make_code_map(&mv, c->v, c, box)) != FA_OK) return rc;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  kern<<<ch.G, 128, L::kSmem, st>>>(mk, mv, a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+}
+
+int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  if (c->d == 128) {
+    if (c->format == FA_KV_INT8)
+      return ch.M == 16 ? launch_narrow<128, fa::kKvInt8, 1>(c, a, ch, st) : launch_narrow<128, fa::kKvInt8, 2>(c, a, ch, st);
+    return ch.M == 16 ? launch_narrow<128, fa::kKvFp8, 1>(c, a, ch, st) : launch_narrow<128, fa::kKvFp8, 2>(c, a, ch, st);
+  }
+  if (c->format == FA_KV_INT8)
+    return ch.M == 16 ? launch_narrow<64, fa::kKvInt8, 1>(c, a, ch, st) : launch_narrow<64, fa::kKvInt8, 2>(c, a, ch, st);
+  return ch.M == 16 ? launch_narrow<64, fa::kKvFp8, 1>(c, a, ch, st) : launch_narrow<64, fa::kKvFp8, 2>(c, a, ch, st);
+}
+
+template <int D>
+int launch_merge_cut(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  // few items: a block for each row of a cut item; many: blocks of eight rows
+  const long long items = (long long)a.B * a.Hkv * (((long long)a.max_q * a.g + ch.M - 1) / ch.M);
+  const unsigned y = items <= 64 ? ch.M : ch.M / 8;
+  const dim3 grid((unsigned)(ch.G - 1), y);
+  if (ch.M == 16) fa::kv_merge_cut_kernel<D, 16><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
+  else fa::kv_merge_cut_kernel<D, 32><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+}
+
+template <int D, int MP, int MS>
+void launch_merge_prefix_as(const fa::KvArgs& pf, const fa::KvArgs& sf, const Choice& cp, const Choice& cs,
+                            cudaStream_t st) {
+  const long long rows = (long long)sf.total * sf.Hq;
+  const unsigned grid = (unsigned)(rows < kSms * 64 ? rows : kSms * 64);
+  fa::kv_merge_prefix_kernel<D, MP, MS><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
+}
+
+template <int D>
+int launch_merge_prefix(const fa::KvArgs& pf, const fa::KvArgs& sf, const Choice& cp, const Choice& cs,
+                        cudaStream_t st) {
+  if (cp.M == 16) launch_merge_prefix_as<D, 16, 16>(pf, sf, cp, cs, st);
+  else if (cs.M == 16) launch_merge_prefix_as<D, 32, 16>(pf, sf, cp, cs, st);
+  else launch_merge_prefix_as<D, 32, 32>(pf, sf, cp, cs, st);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+}
+
+// Checks of sizes that fa_fwd_kvcache and its workspace size share: FA_OK, a negative status, or 1 for nothing to do.
+int check_attend(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len) {
+  if (B < 0 || Hq < 0 || total_q < 0 || max_q < 0 || prefix_len < 0) return FA_ERR_INVALID_ARG;
+  if (Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || Hq == 0 || total_q == 0 || max_q == 0) return 1;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || B > (1 << 24) || total_q > (1 << 24) || max_q > (1 << 24)) return FA_ERR_TOO_LARGE;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv_append(const fa_kv_cache* cache, const void* k, const void* v, const fa_strides* strides,
+                 const int32_t* block_table, int max_pages, int64_t table_stride, const int32_t* starts,
+                 const int32_t* cu_seqlens, int B, int total_tokens, void* stream) {
+  fa::KvArgs a;
+  const int rc = rows_setup(cache, k, v, strides, block_table, max_pages, table_stride, starts, cu_seqlens, B,
+                            total_tokens, &a);
+  if (rc != FA_OK) return rc == 1 ? FA_OK : rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->d == 64 ? launch_rows<64>(a, cache->format, true, st) : launch_rows<128>(a, cache->format, true, st);
+}
+
+int fa_kv_read(const fa_kv_cache* cache, void* k, void* v, const fa_strides* strides, const int32_t* block_table,
+               int max_pages, int64_t table_stride, const int32_t* starts, const int32_t* cu_seqlens, int B,
+               int total_tokens, void* stream) {
+  fa::KvArgs a;
+  const int rc = rows_setup(cache, k, v, strides, block_table, max_pages, table_stride, starts, cu_seqlens, B,
+                            total_tokens, &a);
+  if (rc != FA_OK) return rc == 1 ? FA_OK : rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->d == 64 ? launch_rows<64>(a, cache->format, false, st) : launch_rows<128>(a, cache->format, false, st);
+}
+
+size_t fa_fwd_kvcache_workspace_size(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len) {
+  if (check_attend(B, Hq, Hkv, d, total_q, max_q, prefix_len) != FA_OK) return 0;
+  return layout_of(B, Hq, Hkv, d, total_q, max_q, B > 1 ? prefix_len : 0).bytes;
+}
+
+int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides, const fa_kv_cache* cache,
+                   const int32_t* block_table, int max_pages, int64_t table_stride, const int32_t* seqlens,
+                   const int32_t* cu_seqlens_q, int B, int Hq, int total_q, int max_q, float scale, int causal,
+                   int prefix_len, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache);
+  if (rc != FA_OK) return rc;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  const int Hkv = cache->num_kv_heads, d = cache->d;
+  rc = check_attend(B, Hq, Hkv, d, total_q, max_q, prefix_len);
+  if (rc != FA_OK) return rc == 1 ? FA_OK : rc;
+  if ((rc = check_batch(block_table, max_pages, table_stride, B, total_q)) != FA_OK) return rc;
+  if (prefix_len % cache->page_size != 0 || (long long)prefix_len > (long long)max_pages * cache->page_size)
+    return FA_ERR_INVALID_ARG;
+  if (!cu_seqlens_q && (long long)B * max_q != total_q) return FA_ERR_INVALID_ARG;
+  if (!q || !o || !strides || !seqlens) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens_q, 4))
+    return FA_ERR_ALIGNMENT;
+  if (!tok_strides_ok(strides[0]) || !tok_strides_ok(strides[1])) return FA_ERR_ALIGNMENT;
+  if (B == 1) prefix_len = 0;  // nothing is shared
+  const Layout l = layout_of(B, Hq, Hkv, d, total_q, max_q, prefix_len);
+  if (!workspace || workspace_bytes < l.bytes) return FA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return FA_ERR_ALIGNMENT;
+  char* ws = static_cast<char*>(workspace);
+
+  fa::KvArgs a;
+  fill_cache(&a, cache);
+  a.table = block_table;
+  a.max_pages = max_pages;
+  a.table_stride = table_stride;
+  a.lens = seqlens;
+  a.cu = cu_seqlens_q;
+  a.B = B;
+  a.total = total_q;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.q_sn = strides[0].n;
+  a.q_sh = strides[0].h;
+  a.o_sn = strides[1].n;
+  a.o_sh = strides[1].h;
+  a.lse = lse;
+  a.Hq = Hq;
+  a.g = Hq / Hkv;
+  a.max_q = max_q;
+  a.causal = causal;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.prefix_len = prefix_len;
+  a.err = fa_host::device_error_ptr();
+  if (!a.err) return fa_host::cuda_fail(cudaErrorInvalidSymbol);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (prefix_len == 0) {
+    a.phase = fa::kKvWhole;
+    a.part_o = reinterpret_cast<float*>(ws + l.pw.o);
+    a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
+    if ((rc = launch_phase(cache, a, l.whole, st)) != FA_OK) return rc;
+    return d == 64 ? launch_merge_cut<64>(a, l.whole, st) : launch_merge_cut<128>(a, l.whole, st);
+  }
+  fa::KvArgs pf = a, sf = a;
+  pf.phase = fa::kKvPrefix;
+  pf.part_o = reinterpret_cast<float*>(ws + l.pp.o);
+  pf.part_lse = reinterpret_cast<float*>(ws + l.pp.lse);
+  pf.row_o = reinterpret_cast<float*>(ws + l.prefix_o);
+  pf.row_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
+  sf.phase = fa::kKvSuffix;
+  sf.part_o = reinterpret_cast<float*>(ws + l.ps.o);
+  sf.part_lse = reinterpret_cast<float*>(ws + l.ps.lse);
+  sf.row_o = reinterpret_cast<float*>(ws + l.suffix_o);
+  sf.row_lse = reinterpret_cast<float*>(ws + l.suffix_lse);
+  sf.off = reinterpret_cast<long long*>(ws + l.off);
+  if ((rc = launch_phase(cache, pf, l.prefix, st)) != FA_OK) return rc;
+  if ((rc = launch_phase(cache, sf, l.suffix, st)) != FA_OK) return rc;
+  return d == 64 ? launch_merge_prefix<64>(pf, sf, l.prefix, l.suffix, st)
+                 : launch_merge_prefix<128>(pf, sf, l.prefix, l.suffix, st);
+}
+
+}  // extern "C"

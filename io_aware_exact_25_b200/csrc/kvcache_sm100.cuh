@@ -1,0 +1,754 @@
+// kvcache_sm100.cuh -- the quantised, paged key/value cache: writing it,
+// reading it back, and how attention over it is cut into work.
+//
+// Cache: pages [num_pages, Hkv, page_size, d] of 8-bit codes for K and for V
+// and one fp32 scale per (page, head, slot).  A row x of d values is stored as
+//   int8: scale = amax / 127, code = rint(127 x / amax)
+//   fp8:  scale = amax / 448, code = e4m3(448 x / amax)
+// (round half to even), amax = max |x|, and stands for code * scale.  The
+// position p of sequence b sits in page block_table[b][p / page_size], slot
+// p % page_size.
+#pragma once
+
+#include "debug_check.cuh"
+#include "sm100.cuh"
+
+namespace fa {
+
+enum : int { kKvInt8 = 0, kKvFp8 = 1 };
+constexpr int kDevBadPage = 5;  // a page number outside the cache, or a position past the block table
+
+struct KvArgs {
+  // the cache
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int num_pages, page_shift, Hkv;
+  // the sequences
+  const int* table;  // [B][max_pages], rows table_stride apart
+  long long table_stride;
+  int max_pages;
+  const int* cu;    // token offsets [B + 1] of q (attention) or of the rows (append, read); may be null
+  const int* lens;  // keys per sequence (attention) or first position (append, read; may be null)
+  int B, total;     // sequences; rows of the token-major tensors
+  int* err;
+  // append, read: token-major K and V rows
+  __nv_bfloat16* xk;
+  __nv_bfloat16* xv;
+  long long xk_sn, xk_sh, xv_sn, xv_sh;
+  // attention
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  long long q_sn, q_sh, o_sn, o_sh;
+  float* lse;  // [Hq, total] natural log; may be null
+  int Hq, g;   // query heads; query heads per key head
+  int max_q;   // largest number of query rows of a sequence
+  int causal;
+  float scale_log2;  // scale * log2(e)
+  int prefix_len;    // keys [0, prefix_len) are the batch's shared prefix (0: none)
+  int phase;         // kKvWhole: all keys; kKvPrefix: the shared ones; kKvSuffix: the rest
+  // pieces of items that several CTAs share: slot 2 c + s of CTA c
+  float* part_o;    // [2 G][M][D], normalised
+  float* part_lse;  // [2 G][M], base 2
+  // whole results of a phase, merged afterwards (phases other than kKvWhole)
+  float* row_o;      // [total * Hq][D], normalised
+  float* row_lse;    // [total * Hq], base 2
+  long long* off;    // [B + 1] work units before each sequence
+};
+
+enum : int { kKvWhole = 0, kKvPrefix = 1, kKvSuffix = 2 };
+
+// The sequence that owns token t: the last b with cu[b] <= t, by a 32-ary search of one warp (every lane
+// gets the result; every probe lies in [0, B], whatever cu holds).
+__device__ __forceinline__ int kv_find_seq(const int* cu, int B, int t, int lane) {
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int at = lane * step;
+    const bool le = at < n && __ldg(cu + lo + at) <= t;
+    const int hits = __popc(__ballot_sync(0xffffffffu, le));
+    const int skip = hits > 0 ? (hits - 1) * step : 0;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
+// Row of the cache's [page, head, slot] grid that holds position pos of sequence b and head 0, or -1 (and a
+// device error) where the block table has no such page.  Head h is h << page_shift rows further on.
+__device__ __forceinline__ long long kv_row(const KvArgs& a, int b, long long pos, bool report) {
+  const long long pi = pos >> a.page_shift;
+  int page = -1;
+  if (pos >= 0 && pi < a.max_pages) page = __ldg(a.table + b * a.table_stride + pi);
+  if (page < 0 || page >= a.num_pages) {
+    if (report && a.err) atomicCAS(a.err, kDevOk, kDevBadPage);
+    return -1;
+  }
+  return (((long long)page * a.Hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+}
+
+// --------------------------------------------------------------- rounding
+
+// y rounded to 20 significant bits.  The exact quotient top * x / amax of bf16
+// numbers is either on a border between two codes (a dyadic number of few
+// bits) or further than 2^-16 of its value away from one: with 8-bit integers
+// X, A and a border of M / 2^n, M < 2^8, |top X 2^i - M A| is a whole number of
+// units of which M A is at most 2^16.  y carries a relative error of 2^-23 (a
+// rounded reciprocal, a rounded product), so this rounding puts every border
+// case exactly on its border and moves nothing across one: the code that
+// follows is the exact quotient's, half to even, without a division.
+__device__ __forceinline__ float kv_snap(float y) {
+  return __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_encode4(float y0, float y1, float y2, float y3) {
+  if constexpr (FMT == kKvInt8) {
+    // adding 1.5 * 2^23 rounds half to even and leaves the two's complement
+    // of the whole number in the low byte
+    const uint32_t a = __float_as_uint(__fadd_rn(kv_snap(y0), 12582912.f));
+    const uint32_t b = __float_as_uint(__fadd_rn(kv_snap(y1), 12582912.f));
+    const uint32_t c = __float_as_uint(__fadd_rn(kv_snap(y2), 12582912.f));
+    const uint32_t d = __float_as_uint(__fadd_rn(kv_snap(y3), 12582912.f));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  } else {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(kv_snap(y1)), "f"(kv_snap(y0)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(kv_snap(y3)), "f"(kv_snap(y2)));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void kv_decode4(uint32_t w, float (&x)[4]) {
+  if constexpr (FMT == kKvInt8) {
+    const uint32_t u = w ^ 0x80808080u;  // code + 128 in each byte
+    // 2^23 + byte as a float, minus 2^23 + 128
+    x[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f;
+    x[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f;
+    x[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.f;
+    x[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
+  } else {
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    const float2 p = __half22float2(*reinterpret_cast<__half2*>(&lo));
+    const float2 q = __half22float2(*reinterpret_cast<__half2*>(&hi));
+    x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;
+  }
+}
+
+// ----------------------------------------------------------- append, read
+
+// Append and read share their decomposition.  A cache row of d codes is the
+// work of d / 8 lanes, 16 bytes of bf16 against 8 bytes of codes each, so one
+// warp moves 32 / (d / 8) rows at a time and kKvUnroll times that in one unit,
+// all loads ahead of all stores.  The rows of a token are its Hkv key rows
+// and then its Hkv value rows.  Both directions are bound by memory.
+constexpr int kKvUnroll = 4;
+
+template <int D>
+__host__ __device__ constexpr int kv_rows_per_unit() { return 32 / (D / 8) * kKvUnroll; }
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr float kTop = FMT == kKvInt8 ? 127.f : 448.f;
+  const int lane = threadIdx.x & 31;
+  const int units = (2 * a.Hkv + kv_rows_per_unit<D>() - 1) / kv_rows_per_unit<D>();  // per token
+  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = (int)(w / units);
+  if (t >= a.total) return;
+  const int r0 = (int)(w - (long long)t * units) * kv_rows_per_unit<D>() + lane / LPR;
+  const int col = (lane % LPR) * 8;
+  uint4 x[kKvUnroll];
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; ++u) {
+    const int r = r0 + u * RPW;
+    x[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < 2 * a.Hkv) {
+      const __nv_bfloat16* src = r < a.Hkv ? a.xk + t * a.xk_sn + r * a.xk_sh
+                                           : a.xv + t * a.xv_sn + (r - a.Hkv) * a.xv_sh;
+      x[u] = __ldg(reinterpret_cast<const uint4*>(src + col));
+    }
+  }
+  int b = t, first = t, end = t + 1;
+  if (a.cu) {
+    b = kv_find_seq(a.cu, a.B, t, lane);
+    first = __ldg(a.cu + b);
+    end = __ldg(a.cu + b + 1);
+  }
+  if (t < first || t >= end) return;  // a row of no sequence
+  const long long row = kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
+  if (row < 0) return;
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; ++u) {
+    const int r = r0 + u * RPW;
+    const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+    // the largest |x| as bf16 bits: as integers infinities and NaN sort above all numbers
+    uint32_t m2 = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, xs[i] & 0x7fff7fffu);
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, s));
+    const uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
+    const float amax = __uint_as_float(mb << 16);
+    // tiny rows are lifted by 2^100 so that the reciprocal stays in range
+    const float lift = amax < 7.888609052210118e-31f ? 1.2676506002282294e30f : 1.f;
+    const bool finite = mb < 0x7f80u;
+    const float inv = finite && mb != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[4] = {bf16_lo(xs[2 * i]), bf16_hi(xs[2 * i]), bf16_lo(xs[2 * i + 1]), bf16_hi(xs[2 * i + 1])};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = finite ? y[e] * lift * inv : 0.f;
+      c[i] = kv_encode4<FMT>(y[0], y[1], y[2], y[3]);
+    }
+    if (r < 2 * a.Hkv) {
+      const int h = r < a.Hkv ? r : r - a.Hkv;
+      const long long at = row + ((long long)h << a.page_shift);
+      const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
+      (void)lim;
+      if (FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
+        *reinterpret_cast<uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col) = make_uint2(c[0], c[1]);
+        if (lane % LPR == 0)
+          (r < a.Hkv ? a.ks : a.vs)[at] = finite ? __fdiv_rn(amax, kTop) : __uint_as_float(0x7fc00000u);
+      }
+    }
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) kv_read_kernel(const KvArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31;
+  const int units = (2 * a.Hkv + kv_rows_per_unit<D>() - 1) / kv_rows_per_unit<D>();
+  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = (int)(w / units);
+  if (t >= a.total) return;
+  const int r0 = (int)(w - (long long)t * units) * kv_rows_per_unit<D>() + lane / LPR;
+  const int col = (lane % LPR) * 8;
+  int b = t, first = t, end = t + 1;
+  if (a.cu) {
+    b = kv_find_seq(a.cu, a.B, t, lane);
+    first = __ldg(a.cu + b);
+    end = __ldg(a.cu + b + 1);
+  }
+  if (t < first || t >= end) return;  // a row of no sequence: left as it was
+  const long long row = kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
+  const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
+  (void)lim;
+  uint2 c[kKvUnroll];
+  float sc[kKvUnroll];
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; ++u) {
+    const int r = r0 + u * RPW;
+    const int h = r < a.Hkv ? r : r - a.Hkv;
+    const long long at = row + ((long long)h << a.page_shift);
+    c[u] = make_uint2(0u, 0u);
+    sc[u] = 0.f;
+    if (r < 2 * a.Hkv && row >= 0 && FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
+      c[u] = *reinterpret_cast<const uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col);
+      sc[u] = (r < a.Hkv ? a.ks : a.vs)[at];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; ++u) {
+    const int r = r0 + u * RPW;
+    if (r >= 2 * a.Hkv) continue;
+    float x[4], y[4];
+    kv_decode4<FMT>(c[u].x, x);
+    kv_decode4<FMT>(c[u].y, y);
+    __nv_bfloat16* dst = r < a.Hkv ? a.xk + t * a.xk_sn + r * a.xk_sh : a.xv + t * a.xv_sn + (r - a.Hkv) * a.xv_sh;
+    st_global_v4(dst + col, pack_bf16x2(x[0] * sc[u], x[1] * sc[u]), pack_bf16x2(x[2] * sc[u], x[3] * sc[u]),
+                 pack_bf16x2(y[0] * sc[u], y[1] * sc[u]), pack_bf16x2(y[2] * sc[u], y[3] * sc[u]));
+  }
+}
+
+// ------------------------------------------------------- work of attention
+//
+// An item is the rows of one sequence and key head -- its query tokens times
+// the g query heads of the group, in tiles of M rows -- against the keys they
+// see; its work is counted in units of kKvUnit keys.  The units of all items,
+// sequence by sequence, head by head, tile by tile, form one line that the G
+// CTAs of the grid cut into equal stretches, whatever the lengths: the cut is
+// computed on the device from the lengths, so a captured launch follows them.
+// An item inside one stretch is finished by its CTA; an item that is cut
+// leaves a normalised piece and its logsumexp per CTA, merged afterwards.  A
+// CTA has at most two such pieces, of its first and of its last item.
+constexpr int kKvUnit = 128;
+
+struct KvSeq {
+  int row0, lq, lk;  // first query row, query rows, keys
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, bool report) {
+  KvSeq s;
+  if (a.phase == kKvPrefix) {  // the whole batch as one sequence over the shared keys
+    s.row0 = 0;
+    s.lq = a.total;
+    s.lk = a.prefix_len;
+    return s;
+  }
+  if (a.cu) {
+    const SeqSpan sp = varlen_span(a.cu, nullptr, b, a.total, a.max_q, a.err, report);
+    s.row0 = sp.row0;
+    s.lq = sp.len;
+  } else {
+    s.row0 = b * a.max_q;
+    s.lq = a.max_q;
+  }
+  const int L = __ldg(a.lens + b);
+  const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffffffll - kKvUnit);
+  s.lk = (int)min((long long)max(L, 0), cap);
+  if (report && (L < 0 || L > cap) && a.err) atomicCAS(a.err, kDevOk, kDevBadSeqlens);
+  return s;
+}
+
+// keys that query i (within its sequence) sees: [0, kv_end)
+__device__ __forceinline__ int kv_end(const KvArgs& a, const KvSeq& s, int i) {
+  if (a.phase == kKvPrefix) return s.lk;
+  return a.causal ? min(max(s.lk - s.lq + i + 1, 0), s.lk) : s.lk;
+}
+
+__device__ __forceinline__ int kv_begin(const KvArgs& a) { return a.phase == kKvSuffix ? a.prefix_len : 0; }
+
+// one past the last key that some row of tile rt sees
+template <int M>
+__device__ __forceinline__ int kv_item_end(const KvArgs& a, const KvSeq& s, int rt) {
+  const long long last = min((long long)(rt + 1) * M, (long long)s.lq * a.g) - 1;
+  return kv_end(a, s, (int)(last / a.g));
+}
+
+template <int M>
+__device__ __forceinline__ int kv_tiles(const KvArgs& a, const KvSeq& s) {
+  return (int)(((long long)s.lq * a.g + M - 1) / M);
+}
+
+template <int M>
+__device__ __forceinline__ int kv_item_units(const KvArgs& a, const KvSeq& s, int rt) {
+  const int keys = kv_item_end<M>(a, s, rt) - kv_begin(a);
+  return max(1, (keys + kKvUnit - 1) / kKvUnit);  // an item without keys still writes its rows
+}
+
+// units of one key head of the sequence
+template <int M>
+__device__ __forceinline__ long long kv_head_units(const KvArgs& a, const KvSeq& s) {
+  const int nt = kv_tiles<M>(a, s);
+  if (nt == 0) return 0;
+  if (nt == 1 || !a.causal || a.phase == kKvPrefix) return (long long)nt * kv_item_units<M>(a, s, nt - 1);
+  long long n = 0;
+  for (int rt = 0; rt < nt; ++rt) n += kv_item_units<M>(a, s, rt);
+  return n;
+}
+
+__device__ __forceinline__ int kv_num_seqs(const KvArgs& a) { return a.phase == kKvPrefix ? 1 : a.B; }
+
+// First unit of CTA c's stretch, and the CTA whose stretch holds unit u.  G is the number of stretches: the grid,
+// or one per unit where there are fewer units than CTAs, so none is empty.
+__device__ __forceinline__ long long kv_cut(long long W, int G, int c) { return W * c / G; }
+__device__ __forceinline__ int kv_cta_of(long long W, int G, long long u) { return (int)(((u + 1) * G - 1) / W); }
+
+// A place on the line of units: unit `unit` of row tile rt of head h of sequence b.
+struct KvPlace {
+  int b, h, rt, unit;
+};
+
+// Scratch of kv_place.
+struct KvScan {
+  long long warp_sum[32];
+  long long place[2];
+};
+
+// Inclusive sum over the block (NT threads) and its total.
+template <int NT>
+__device__ __forceinline__ long long kv_block_inclusive(long long x, KvScan* sc, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sc->warp_sum[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    const long long v = sc->warp_sum[i];
+    if (i < warp) before += v;
+    all += v;
+  }
+  *total = all;
+  return before + x;
+}
+
+// The line's length W, and the sequence that holds the first unit of CTA c (and the units before it within the
+// sequence), by the whole block.  Returns W and clamps G to the stretches there are; *b < 0 if CTA c has none.
+// In the suffix phase CTA 0 also records every sequence's first unit.
+template <int M, int NT>
+__device__ __forceinline__ long long kv_place(const KvArgs& a, int c, int& G, KvScan* sc, int* b, long long* rem,
+                                              bool report) {
+  const int n = kv_num_seqs(a);
+  auto units_of = [&](int i, bool rep) -> long long {
+    if (i >= n) return 0;
+    const KvSeq s = kv_seq(a, i, rep);
+    return kv_head_units<M>(a, s) * a.Hkv;
+  };
+  long long* off = c == 0 && a.off && a.phase == kKvSuffix ? a.off : nullptr;
+  const long long mine = units_of((int)threadIdx.x, report);  // the first NT sequences' units stay in registers
+  long long W = 0, part = 0;
+  long long first_incl = kv_block_inclusive<NT>(mine, sc, &part);
+  W = part;
+  if (n > NT) {
+    long long sum = 0;
+    for (int i = NT + threadIdx.x; i < n; i += NT) sum += units_of(i, report);
+    long long rest;
+    (void)kv_block_inclusive<NT>(sum, sc, &rest);
+    W += rest;
+  }
+  G = (int)min((long long)G, W);
+  const long long u0 = c < G ? kv_cut(W, G, c) : W;
+  *b = -1;
+  *rem = 0;
+  if (c >= G && !off) return W;
+  __syncthreads();
+  long long run = 0;
+  bool found = false;
+  for (int base = 0; base < n; base += NT) {
+    const int i = base + threadIdx.x;
+    long long x = mine, incl = first_incl, tot = part;
+    if (base > 0) {
+      x = units_of(i, false);
+      incl = kv_block_inclusive<NT>(x, sc, &tot);
+    }
+    if (off && i < n) off[i] = run + incl - x;
+    const long long lo = run + incl - x;
+    if (!found && u0 >= lo && u0 < lo + x) {
+      sc->place[0] = i;
+      sc->place[1] = u0 - lo;
+    }
+    if (!found && u0 < run + tot) {
+      found = true;
+      __syncthreads();
+      *b = (int)sc->place[0];
+      *rem = sc->place[1];
+      if (!off) break;
+    }
+    run += tot;
+  }
+  if (off && threadIdx.x == 0) off[n] = W;
+  return W;
+}
+
+// The place `rem` units into sequence b.
+template <int M>
+__device__ __forceinline__ KvPlace kv_within(const KvArgs& a, const KvSeq& s, int b, long long rem) {
+  KvPlace p;
+  p.b = b;
+  const long long per = kv_head_units<M>(a, s);
+  p.h = (int)(rem / per);
+  rem -= p.h * per;
+  p.rt = 0;
+  const int nt = kv_tiles<M>(a, s);
+  if (nt > 1 && (!a.causal || a.phase == kKvPrefix)) {
+    const int n = kv_item_units<M>(a, s, 0);
+    p.rt = (int)(rem / n);
+    rem -= (long long)p.rt * n;
+  } else {
+    for (; p.rt + 1 < nt; ++p.rt) {
+      const int n = kv_item_units<M>(a, s, p.rt);
+      if (rem < n) break;
+      rem -= n;
+    }
+  }
+  p.unit = (int)rem;
+  return p;
+}
+
+// The item after p; false at the end of the line.  Updates s when the sequence changes.
+template <int M>
+__device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
+  p.unit = 0;
+  if (++p.rt < kv_tiles<M>(a, s)) return true;
+  p.rt = 0;
+  if (++p.h < a.Hkv) return true;
+  p.h = 0;
+  const int n = kv_num_seqs(a);
+  while (++p.b < n) {
+    s = kv_seq(a, p.b, false);
+    if (s.lq > 0) return true;
+  }
+  return false;
+}
+
+// Where a row of an item lives: token, query head, and how many keys it sees.
+struct KvRow {
+  int token, head, end;
+};
+
+template <int M>
+__device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
+  KvRow x;
+  const long long rr = (long long)rt * M + r;
+  if (rr >= (long long)s.lq * a.g) return KvRow{-1, 0, 0};
+  const int i = (int)(rr / a.g);
+  x.token = s.row0 + i;
+  x.head = h * a.g + (int)(rr - (long long)i * a.g);
+  x.end = kv_end(a, s, i);
+  if (a.phase == kKvPrefix) {
+    // the token's own sequence bounds what it sees of the prefix
+    int b = 0, first = 0, lq = a.max_q;
+    if (a.cu) {
+      int lo = 0, hi = a.B;  // last b with cu[b] <= token
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.cu + mid) <= x.token) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      const SeqSpan sp = varlen_span(a.cu, nullptr, b, a.total, a.max_q, nullptr, false);
+      first = sp.row0;
+      lq = sp.len;
+    } else {
+      b = i / a.max_q;
+      first = b * a.max_q;
+    }
+    const int at = x.token - first;
+    if (at < 0 || at >= lq) return KvRow{-1, 0, 0};  // a row of no sequence
+    const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffffffll - kKvUnit);
+    const int L = (int)min((long long)max(__ldg(a.lens + b), 0), cap);
+    x.end = min(s.lk, a.causal ? max(L - lq + at + 1, 0) : L);
+  }
+  return x;
+}
+
+// Columns [col0, col0 + NC) of a row's normalised result, to where the phase wants it: the output (a finished row
+// of a kKvWhole launch), the phase's result rows (a finished row otherwise), or a piece.
+template <int D, int NC>
+__device__ __forceinline__ void kv_put_row(const KvArgs& a, const KvRow& x, bool whole, long long piece,
+                                           long long pieces, int col0, const float (&v)[NC], float lse2) {
+  static_assert(NC % 8 == 0, "16-byte stores");
+  if (whole && a.phase == kKvWhole) {
+    const long long at = x.token * a.o_sn + x.head * a.o_sh;
+    if (FA_IN(kSiteKvO, at, D, extent4(1, a.Hq, a.total, D, 0, a.o_sh, a.o_sn), a.err)) {
+#pragma unroll
+      for (int e = 0; e < NC; e += 8)
+        st_global_v4(a.o + at + col0 + e, pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                     pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+    }
+    const long long la = (long long)x.head * a.total + x.token;
+    if (col0 == 0 && a.lse && FA_IN(kSiteKvLse, la, 1, (long long)a.Hq * a.total, a.err))
+      a.lse[la] = lse2 * 0.69314718055994531f;
+    return;
+  }
+  const long long row = whole ? (long long)x.token * a.Hq + x.head : piece;
+  const long long lim = whole ? (long long)a.total * a.Hq : pieces;
+  (void)lim;
+  if (!FA_IN(kSiteKvPart, row, 1, lim, a.err)) return;
+  float* dst = (whole ? a.row_o : a.part_o) + row * D + col0;
+#pragma unroll
+  for (int e = 0; e < NC; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  if (col0 == 0) (whole ? a.row_lse : a.part_lse)[row] = lse2;
+}
+
+// ------------------------------------------------------------------ merge
+
+constexpr int kKvMergeThreads = 256;
+
+template <int D>
+__device__ __forceinline__ void kv_axpy(float (&acc)[D / 32], float w, const float* src) {
+  if constexpr (D == 128) {
+    const float4 v = *reinterpret_cast<const float4*>(src);
+    acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(src);
+    acc[0] += w * v.x, acc[1] += w * v.y;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void kv_store_row(const KvArgs& a, const KvRow& x, int lane, const float (&v)[D / 32],
+                                             float lse2) {
+  const long long at = x.token * a.o_sn + x.head * a.o_sh;
+  if (FA_IN(kSiteKvO, at, D, extent4(1, a.Hq, a.total, D, 0, a.o_sh, a.o_sn), a.err)) {
+    __nv_bfloat16* dst = a.o + at + lane * (D / 32);
+    if constexpr (D == 128)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(v[0], v[1]);
+  }
+  if (lane == 0 && a.lse &&
+      FA_IN(kSiteKvLse, (long long)x.head * a.total + x.token, 1, (long long)a.Hq * a.total, a.err))
+    a.lse[(long long)x.head * a.total + x.token] = lse2 * 0.69314718055994531f;
+}
+
+// weight of a piece against the largest logsumexp mx of its row (pieces of no keys weigh nothing; NaN stays)
+__device__ __forceinline__ float kv_weight(float lse2, float mx) {
+  return lse2 == -INFINITY ? 0.f : exp2f(lse2 - mx);
+}
+
+// A piece list of one row: base points at the row in the piece of CTA c0 (slot slot0), the next CTAs' first slots
+// follow.  A finished row of a phase is a list of one.
+struct KvPieces {
+  const float* o;
+  const float* lse;
+  int n;
+  long long first;   // row of the first piece
+  long long second;  // row of the second piece; the others follow `stride` rows apart
+  long long stride;
+  __device__ __forceinline__ long long at(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
+};
+
+// The pieces of row r of the item of n units that starts at unit w0.
+template <int M>
+__device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, long long W, int G, long long w0, int n, int r) {
+  const int c0 = kv_cta_of(W, G, w0), c1 = kv_cta_of(W, G, w0 + n - 1);
+  const int slot0 = w0 > kv_cut(W, G, c0) ? 1 : 0;
+  KvPieces p;
+  p.o = a.part_o;
+  p.lse = a.part_lse;
+  p.n = c1 - c0 + 1;
+  p.first = (2ll * c0 + slot0) * M + r;
+  p.second = (2ll * c0 + 2) * M + r;
+  p.stride = 2ll * M;
+  return p;
+}
+
+// Merge of up to two piece lists into row x by `group` warps (1, or all NW of the block; then every warp of the
+// block calls it for the same row):
+//   lse = log2 sum_s 2^lse_s,  O = sum_s 2^(lse_s - lse) O_s
+template <int NW, int D>
+struct KvMergeSmem {
+  float mx[NW], sum[NW], o[NW][D];
+};
+
+template <int D>
+__device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces (&p)[2], int group,
+                             KvMergeSmem<kKvMergeThreads / 32, D>& sm) {
+  constexpr int NW = kKvMergeThreads / 32, PER = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int me = group == 1 ? 0 : warp;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int l = 0; l < 2; ++l)
+    for (int k = lane; k < p[l].n; k += 32) mx = fmaxf(mx, p[l].lse[p[l].at(k)]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  float acc[PER] = {}, sum = 0.f;
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+#pragma unroll 4
+    for (int k = me; k < p[l].n; k += group) {
+      const long long at = p[l].at(k);
+      const float wt = kv_weight(p[l].lse[at], mx);
+      sum += wt;
+      kv_axpy<D>(acc, wt, p[l].o + at * D + lane * PER);
+    }
+  }
+  if (group > 1) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) sm.o[warp][lane * PER + e] = acc[e];
+    if (lane == 0) sm.sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        sum += sm.sum[i];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] += sm.o[i][lane * PER + e];
+      }
+    }
+  }
+  if (me == 0) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= inv;
+    kv_store_row<D>(a, x, lane, acc, sum == 0.f ? -INFINITY : mx + log2f(sum));
+  }
+  if (group > 1) __syncthreads();
+}
+
+// Items that the stretches cut.  Block (c, y) looks at the cut before CTA
+// c + 1; if that is the first cut inside an item, the blocks of that c merge
+// the item's rows, a warp a row, or with more than eight pieces the block a
+// row with the pieces spread over its warps (one key head's 64K keys leave
+// over a hundred pieces, a chain that one warp would walk alone).
+template <int D, int M>
+__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvArgs a, int G) {
+  constexpr int NW = kKvMergeThreads / 32;
+  __shared__ KvScan sc;
+  __shared__ KvMergeSmem<NW, D> sm;
+  const int warp = threadIdx.x >> 5;
+  const int c = (int)blockIdx.x + 1;
+  int b;
+  long long rem;
+  const long long W = kv_place<M, kKvMergeThreads>(a, c, G, &sc, &b, &rem, false);
+  if (b < 0) return;
+  const KvSeq s = kv_seq(a, b, false);
+  const KvPlace at = kv_within<M>(a, s, b, rem);
+  if (at.unit == 0) return;  // the cut falls between two items
+  const long long w0 = kv_cut(W, G, c) - at.unit;
+  if (kv_cta_of(W, G, w0) != c - 1) return;  // not the item's first cut
+  const int n = kv_item_units<M>(a, s, at.rt);
+  const int group = kv_pieces<M>(a, W, G, w0, n, 0).n > NW ? NW : 1;
+  const int rows = group == 1 ? NW : 1;  // rows a block merges at a time
+  for (int r0 = blockIdx.y * rows; r0 < M; r0 += gridDim.y * rows) {
+    const int r = r0 + (group == 1 ? warp : 0);
+    const KvRow x = kv_row_of<M>(a, s, at.h, at.rt, r);
+    if (r >= M || x.token < 0) continue;
+    KvPieces p[2];
+    p[0] = kv_pieces<M>(a, W, G, w0, n, r);
+    p[1] = p[0];
+    p[1].n = 0;
+    kv_merge_row<D>(a, x, p, group, sm);
+  }
+}
+
+// Shared prefix: every row's result over the prefix (pf: phase kKvPrefix) and over its own keys (sf: kKvSuffix),
+// each finished or in pieces.  One block a row.
+template <int D, int MP, int MS>
+__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const KvArgs pf, const KvArgs sf, int GP,
+                                                                          int GS) {
+  __shared__ KvMergeSmem<kKvMergeThreads / 32, D> sm;
+  const int lane = threadIdx.x & 31;
+  const KvSeq ps = kv_seq(pf, 0, false);
+  const long long WP = kv_head_units<MP>(pf, ps) * pf.Hkv;
+  const long long WS = sf.off[sf.B];
+  GP = (int)min((long long)GP, WP);
+  GS = (int)min((long long)GS, WS);
+  const long long rows = (long long)sf.total * sf.Hq;
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int t = (int)(row / sf.Hq), head = (int)(row - (long long)t * sf.Hq);
+    const int h = head / sf.g;
+    int b = sf.cu ? kv_find_seq(sf.cu, sf.B, t, lane) : t / sf.max_q;
+    const KvSeq ss = kv_seq(sf, b, false);
+    const int i = t - ss.row0;
+    if (i < 0 || i >= ss.lq) continue;  // a row of no sequence
+    const KvRow x{t, head, 0};
+    KvPieces p[2];
+    {
+      const long long rr = (long long)t * pf.g + (head - h * pf.g);
+      const int rt = (int)(rr / MP), n = kv_item_units<MP>(pf, ps, rt);
+      const long long w0 = ((long long)h * kv_tiles<MP>(pf, ps) + rt) * n;
+      p[0] = kv_pieces<MP>(pf, WP, GP, w0, n, (int)(rr - (long long)rt * MP));
+      if (p[0].n == 1) p[0].o = pf.row_o, p[0].lse = pf.row_lse, p[0].first = row;
+    }
+    {
+      const long long rr = (long long)i * sf.g + (head - h * sf.g);
+      const int rt = (int)(rr / MS), n = kv_item_units<MS>(sf, ss, rt);
+      long long w0 = sf.off[b] + h * kv_head_units<MS>(sf, ss);
+      for (int k = 0; k < rt; ++k) w0 += kv_item_units<MS>(sf, ss, k);
+      p[1] = kv_pieces<MS>(sf, WS, GS, w0, n, (int)(rr - (long long)rt * MS));
+      if (p[1].n == 1) p[1].o = sf.row_o, p[1].lse = sf.row_lse, p[1].first = row;
+    }
+    kv_merge_row<D>(sf, x, p, kKvMergeThreads / 32, sm);
+  }
+}
+
+}  // namespace fa
