@@ -14,6 +14,7 @@
 #include "host.h"
 #include "kvcache_sm100.cuh"
 #include "kvnarrow_sm100.cuh"
+#include "kvwide_sm100.cuh"
 
 namespace {
 
@@ -155,7 +156,8 @@ struct Choice {
 
 Choice choose(long long rows, int d) {
   if (rows <= 16) return {16, kSms * (d == 128 ? NarrowOf<128, 1>::L::kCtasPerSm : NarrowOf<64, 1>::L::kCtasPerSm)};
-  return {32, kSms * (d == 128 ? NarrowOf<128, 2>::L::kCtasPerSm : NarrowOf<64, 2>::L::kCtasPerSm)};
+  if (rows <= 32) return {32, kSms * (d == 128 ? NarrowOf<128, 2>::L::kCtasPerSm : NarrowOf<64, 2>::L::kCtasPerSm)};
+  return {256, kSms};
 }
 
 struct Pieces {
@@ -219,43 +221,51 @@ int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, c
   return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
-int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
-  if (c->d == 128) {
-    if (c->format == FA_KV_INT8)
-      return ch.M == 16 ? launch_narrow<128, fa::kKvInt8, 1>(c, a, ch, st) : launch_narrow<128, fa::kKvInt8, 2>(c, a, ch, st);
-    return ch.M == 16 ? launch_narrow<128, fa::kKvFp8, 1>(c, a, ch, st) : launch_narrow<128, fa::kKvFp8, 2>(c, a, ch, st);
-  }
-  if (c->format == FA_KV_INT8)
-    return ch.M == 16 ? launch_narrow<64, fa::kKvInt8, 1>(c, a, ch, st) : launch_narrow<64, fa::kKvInt8, 2>(c, a, ch, st);
-  return ch.M == 16 ? launch_narrow<64, fa::kKvFp8, 1>(c, a, ch, st) : launch_narrow<64, fa::kKvFp8, 2>(c, a, ch, st);
+template <int D, int FMT>
+int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  using L = fa::KvWideLayout<D>;
+  auto kern = fa::kv_wide_kernel<D, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  kern<<<ch.G, L::kThreads, L::kSmem, st>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
-template <int D>
-int launch_merge_cut(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
-  // few items: a block for each row of a cut item; many: blocks of eight rows
+template <int D, int FMT>
+int launch_phase_as(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  if (ch.M == 16) return launch_narrow<D, FMT, 1>(c, a, ch, st);
+  if (ch.M == 32) return launch_narrow<D, FMT, 2>(c, a, ch, st);
+  return launch_wide<D, FMT>(a, ch, st);
+}
+
+int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
+  if (c->d == 128)
+    return c->format == FA_KV_INT8 ? launch_phase_as<128, fa::kKvInt8>(c, a, ch, st)
+                                   : launch_phase_as<128, fa::kKvFp8>(c, a, ch, st);
+  return c->format == FA_KV_INT8 ? launch_phase_as<64, fa::kKvInt8>(c, a, ch, st)
+                                 : launch_phase_as<64, fa::kKvFp8>(c, a, ch, st);
+}
+
+int launch_merge_cut(const fa::KvArgs& a, int d, const Choice& ch, cudaStream_t st) {
+  if (ch.G < 2) return FA_OK;
+  // Few items: a block for each row of a cut item, which may be in many pieces.  Many items: few blocks a cut, each
+  // walking the item's rows, so that the blocks that find nothing to do stay few.
   const long long items = (long long)a.B * a.Hkv * (((long long)a.max_q * a.g + ch.M - 1) / ch.M);
-  const unsigned y = items <= 64 ? ch.M : ch.M / 8;
+  const unsigned y = items <= 64 ? (ch.M < 64 ? ch.M : 64) : (ch.M + 31) / 32;
   const dim3 grid((unsigned)(ch.G - 1), y);
-  if (ch.M == 16) fa::kv_merge_cut_kernel<D, 16><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
-  else fa::kv_merge_cut_kernel<D, 32><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
+  if (d == 64) fa::kv_merge_cut_kernel<64><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
+  else fa::kv_merge_cut_kernel<128><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
-template <int D, int MP, int MS>
-void launch_merge_prefix_as(const fa::KvArgs& pf, const fa::KvArgs& sf, const Choice& cp, const Choice& cs,
-                            cudaStream_t st) {
+int launch_merge_prefix(const fa::KvArgs& pf, const fa::KvArgs& sf, int d, const Choice& cp, const Choice& cs,
+                        cudaStream_t st) {
   const long long rows = (long long)sf.total * sf.Hq;
   const unsigned grid = (unsigned)(rows < kSms * 64 ? rows : kSms * 64);
-  fa::kv_merge_prefix_kernel<D, MP, MS><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
-}
-
-template <int D>
-int launch_merge_prefix(const fa::KvArgs& pf, const fa::KvArgs& sf, const Choice& cp, const Choice& cs,
-                        cudaStream_t st) {
-  if (cp.M == 16) launch_merge_prefix_as<D, 16, 16>(pf, sf, cp, cs, st);
-  else if (cs.M == 16) launch_merge_prefix_as<D, 32, 16>(pf, sf, cp, cs, st);
-  else launch_merge_prefix_as<D, 32, 32>(pf, sf, cp, cs, st);
+  if (d == 64) fa::kv_merge_prefix_kernel<64><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
+  else fa::kv_merge_prefix_kernel<128><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
@@ -353,18 +363,21 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (prefix_len == 0) {
     a.phase = fa::kKvWhole;
+    a.M = l.whole.M;
     a.part_o = reinterpret_cast<float*>(ws + l.pw.o);
     a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
     if ((rc = launch_phase(cache, a, l.whole, st)) != FA_OK) return rc;
-    return d == 64 ? launch_merge_cut<64>(a, l.whole, st) : launch_merge_cut<128>(a, l.whole, st);
+    return launch_merge_cut(a, d, l.whole, st);
   }
   fa::KvArgs pf = a, sf = a;
   pf.phase = fa::kKvPrefix;
+  pf.M = l.prefix.M;
   pf.part_o = reinterpret_cast<float*>(ws + l.pp.o);
   pf.part_lse = reinterpret_cast<float*>(ws + l.pp.lse);
   pf.row_o = reinterpret_cast<float*>(ws + l.prefix_o);
   pf.row_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
   sf.phase = fa::kKvSuffix;
+  sf.M = l.suffix.M;
   sf.part_o = reinterpret_cast<float*>(ws + l.ps.o);
   sf.part_lse = reinterpret_cast<float*>(ws + l.ps.lse);
   sf.row_o = reinterpret_cast<float*>(ws + l.suffix_o);
@@ -372,8 +385,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   sf.off = reinterpret_cast<long long*>(ws + l.off);
   if ((rc = launch_phase(cache, pf, l.prefix, st)) != FA_OK) return rc;
   if ((rc = launch_phase(cache, sf, l.suffix, st)) != FA_OK) return rc;
-  return d == 64 ? launch_merge_prefix<64>(pf, sf, l.prefix, l.suffix, st)
-                 : launch_merge_prefix<128>(pf, sf, l.prefix, l.suffix, st);
+  return launch_merge_prefix(pf, sf, d, l.prefix, l.suffix, st);
 }
 
 }  // extern "C"

@@ -46,6 +46,7 @@ struct KvArgs {
   int max_q;   // largest number of query rows of a sequence
   int causal;
   float scale_log2;  // scale * log2(e)
+  int M;             // rows of an item tile
   int prefix_len;    // keys [0, prefix_len) are the batch's shared prefix (0: none)
   int phase;         // kKvWhole: all keys; kKvPrefix: the shared ones; kKvSuffix: the rest
   // pieces of items that several CTAs share: slot 2 c + s of CTA c
@@ -316,31 +317,27 @@ __device__ __forceinline__ int kv_end(const KvArgs& a, const KvSeq& s, int i) {
 __device__ __forceinline__ int kv_begin(const KvArgs& a) { return a.phase == kKvSuffix ? a.prefix_len : 0; }
 
 // one past the last key that some row of tile rt sees
-template <int M>
 __device__ __forceinline__ int kv_item_end(const KvArgs& a, const KvSeq& s, int rt) {
-  const long long last = min((long long)(rt + 1) * M, (long long)s.lq * a.g) - 1;
+  const long long last = min((long long)(rt + 1) * a.M, (long long)s.lq * a.g) - 1;
   return kv_end(a, s, (int)(last / a.g));
 }
 
-template <int M>
 __device__ __forceinline__ int kv_tiles(const KvArgs& a, const KvSeq& s) {
-  return (int)(((long long)s.lq * a.g + M - 1) / M);
+  return (int)(((long long)s.lq * a.g + a.M - 1) / a.M);
 }
 
-template <int M>
 __device__ __forceinline__ int kv_item_units(const KvArgs& a, const KvSeq& s, int rt) {
-  const int keys = kv_item_end<M>(a, s, rt) - kv_begin(a);
+  const int keys = kv_item_end(a, s, rt) - kv_begin(a);
   return max(1, (keys + kKvUnit - 1) / kKvUnit);  // an item without keys still writes its rows
 }
 
 // units of one key head of the sequence
-template <int M>
 __device__ __forceinline__ long long kv_head_units(const KvArgs& a, const KvSeq& s) {
-  const int nt = kv_tiles<M>(a, s);
+  const int nt = kv_tiles(a, s);
   if (nt == 0) return 0;
-  if (nt == 1 || !a.causal || a.phase == kKvPrefix) return (long long)nt * kv_item_units<M>(a, s, nt - 1);
+  if (nt == 1 || !a.causal || a.phase == kKvPrefix) return (long long)nt * kv_item_units(a, s, nt - 1);
   long long n = 0;
-  for (int rt = 0; rt < nt; ++rt) n += kv_item_units<M>(a, s, rt);
+  for (int rt = 0; rt < nt; ++rt) n += kv_item_units(a, s, rt);
   return n;
 }
 
@@ -388,14 +385,14 @@ __device__ __forceinline__ long long kv_block_inclusive(long long x, KvScan* sc,
 // The line's length W, and the sequence that holds the first unit of CTA c (and the units before it within the
 // sequence), by the whole block.  Returns W and clamps G to the stretches there are; *b < 0 if CTA c has none.
 // In the suffix phase CTA 0 also records every sequence's first unit.
-template <int M, int NT>
+template <int NT>
 __device__ __forceinline__ long long kv_place(const KvArgs& a, int c, int& G, KvScan* sc, int* b, long long* rem,
                                               bool report) {
   const int n = kv_num_seqs(a);
   auto units_of = [&](int i, bool rep) -> long long {
     if (i >= n) return 0;
     const KvSeq s = kv_seq(a, i, rep);
-    return kv_head_units<M>(a, s) * a.Hkv;
+    return kv_head_units(a, s) * a.Hkv;
   };
   long long* off = c == 0 && a.off && a.phase == kKvSuffix ? a.off : nullptr;
   const long long mine = units_of((int)threadIdx.x, report);  // the first NT sequences' units stay in registers
@@ -444,22 +441,21 @@ __device__ __forceinline__ long long kv_place(const KvArgs& a, int c, int& G, Kv
 }
 
 // The place `rem` units into sequence b.
-template <int M>
 __device__ __forceinline__ KvPlace kv_within(const KvArgs& a, const KvSeq& s, int b, long long rem) {
   KvPlace p;
   p.b = b;
-  const long long per = kv_head_units<M>(a, s);
+  const long long per = kv_head_units(a, s);
   p.h = (int)(rem / per);
   rem -= p.h * per;
   p.rt = 0;
-  const int nt = kv_tiles<M>(a, s);
+  const int nt = kv_tiles(a, s);
   if (nt > 1 && (!a.causal || a.phase == kKvPrefix)) {
-    const int n = kv_item_units<M>(a, s, 0);
+    const int n = kv_item_units(a, s, 0);
     p.rt = (int)(rem / n);
     rem -= (long long)p.rt * n;
   } else {
     for (; p.rt + 1 < nt; ++p.rt) {
-      const int n = kv_item_units<M>(a, s, p.rt);
+      const int n = kv_item_units(a, s, p.rt);
       if (rem < n) break;
       rem -= n;
     }
@@ -469,10 +465,9 @@ __device__ __forceinline__ KvPlace kv_within(const KvArgs& a, const KvSeq& s, in
 }
 
 // The item after p; false at the end of the line.  Updates s when the sequence changes.
-template <int M>
 __device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
   p.unit = 0;
-  if (++p.rt < kv_tiles<M>(a, s)) return true;
+  if (++p.rt < kv_tiles(a, s)) return true;
   p.rt = 0;
   if (++p.h < a.Hkv) return true;
   p.h = 0;
@@ -489,10 +484,9 @@ struct KvRow {
   int token, head, end;
 };
 
-template <int M>
 __device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
   KvRow x;
-  const long long rr = (long long)rt * M + r;
+  const long long rr = (long long)rt * a.M + r;
   if (rr >= (long long)s.lq * a.g) return KvRow{-1, 0, 0};
   const int i = (int)(rr / a.g);
   x.token = s.row0 + i;
@@ -603,7 +597,6 @@ struct KvPieces {
 };
 
 // The pieces of row r of the item of n units that starts at unit w0.
-template <int M>
 __device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, long long W, int G, long long w0, int n, int r) {
   const int c0 = kv_cta_of(W, G, w0), c1 = kv_cta_of(W, G, w0 + n - 1);
   const int slot0 = w0 > kv_cut(W, G, c0) ? 1 : 0;
@@ -611,9 +604,9 @@ __device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, long long W, int 
   p.o = a.part_o;
   p.lse = a.part_lse;
   p.n = c1 - c0 + 1;
-  p.first = (2ll * c0 + slot0) * M + r;
-  p.second = (2ll * c0 + 2) * M + r;
-  p.stride = 2ll * M;
+  p.first = (2ll * c0 + slot0) * a.M + r;
+  p.second = (2ll * c0 + 2) * a.M + r;
+  p.stride = 2ll * a.M;
   return p;
 }
 
@@ -679,7 +672,7 @@ __device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces (&p
 // the item's rows, a warp a row, or with more than eight pieces the block a
 // row with the pieces spread over its warps (one key head's 64K keys leave
 // over a hundred pieces, a chain that one warp would walk alone).
-template <int D, int M>
+template <int D>
 __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvArgs a, int G) {
   constexpr int NW = kKvMergeThreads / 32;
   __shared__ KvScan sc;
@@ -688,22 +681,22 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
   const int c = (int)blockIdx.x + 1;
   int b;
   long long rem;
-  const long long W = kv_place<M, kKvMergeThreads>(a, c, G, &sc, &b, &rem, false);
+  const long long W = kv_place<kKvMergeThreads>(a, c, G, &sc, &b, &rem, false);
   if (b < 0) return;
   const KvSeq s = kv_seq(a, b, false);
-  const KvPlace at = kv_within<M>(a, s, b, rem);
+  const KvPlace at = kv_within(a, s, b, rem);
   if (at.unit == 0) return;  // the cut falls between two items
   const long long w0 = kv_cut(W, G, c) - at.unit;
   if (kv_cta_of(W, G, w0) != c - 1) return;  // not the item's first cut
-  const int n = kv_item_units<M>(a, s, at.rt);
-  const int group = kv_pieces<M>(a, W, G, w0, n, 0).n > NW ? NW : 1;
+  const int n = kv_item_units(a, s, at.rt);
+  const int group = kv_pieces(a, W, G, w0, n, 0).n > NW ? NW : 1;
   const int rows = group == 1 ? NW : 1;  // rows a block merges at a time
-  for (int r0 = blockIdx.y * rows; r0 < M; r0 += gridDim.y * rows) {
+  for (int r0 = blockIdx.y * rows; r0 < a.M; r0 += gridDim.y * rows) {
     const int r = r0 + (group == 1 ? warp : 0);
-    const KvRow x = kv_row_of<M>(a, s, at.h, at.rt, r);
-    if (r >= M || x.token < 0) continue;
+    const KvRow x = kv_row_of(a, s, at.h, at.rt, r);
+    if (r >= a.M || x.token < 0) continue;
     KvPieces p[2];
-    p[0] = kv_pieces<M>(a, W, G, w0, n, r);
+    p[0] = kv_pieces(a, W, G, w0, n, r);
     p[1] = p[0];
     p[1].n = 0;
     kv_merge_row<D>(a, x, p, group, sm);
@@ -712,13 +705,13 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
 
 // Shared prefix: every row's result over the prefix (pf: phase kKvPrefix) and over its own keys (sf: kKvSuffix),
 // each finished or in pieces.  One block a row.
-template <int D, int MP, int MS>
+template <int D>
 __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const KvArgs pf, const KvArgs sf, int GP,
                                                                           int GS) {
   __shared__ KvMergeSmem<kKvMergeThreads / 32, D> sm;
   const int lane = threadIdx.x & 31;
   const KvSeq ps = kv_seq(pf, 0, false);
-  const long long WP = kv_head_units<MP>(pf, ps) * pf.Hkv;
+  const long long WP = kv_head_units(pf, ps) * pf.Hkv;
   const long long WS = sf.off[sf.B];
   GP = (int)min((long long)GP, WP);
   GS = (int)min((long long)GS, WS);
@@ -734,17 +727,17 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const 
     KvPieces p[2];
     {
       const long long rr = (long long)t * pf.g + (head - h * pf.g);
-      const int rt = (int)(rr / MP), n = kv_item_units<MP>(pf, ps, rt);
-      const long long w0 = ((long long)h * kv_tiles<MP>(pf, ps) + rt) * n;
-      p[0] = kv_pieces<MP>(pf, WP, GP, w0, n, (int)(rr - (long long)rt * MP));
+      const int rt = (int)(rr / pf.M), n = kv_item_units(pf, ps, rt);
+      const long long w0 = ((long long)h * kv_tiles(pf, ps) + rt) * n;
+      p[0] = kv_pieces(pf, WP, GP, w0, n, (int)(rr - (long long)rt * pf.M));
       if (p[0].n == 1) p[0].o = pf.row_o, p[0].lse = pf.row_lse, p[0].first = row;
     }
     {
       const long long rr = (long long)i * sf.g + (head - h * sf.g);
-      const int rt = (int)(rr / MS), n = kv_item_units<MS>(sf, ss, rt);
-      long long w0 = sf.off[b] + h * kv_head_units<MS>(sf, ss);
-      for (int k = 0; k < rt; ++k) w0 += kv_item_units<MS>(sf, ss, k);
-      p[1] = kv_pieces<MS>(sf, WS, GS, w0, n, (int)(rr - (long long)rt * MS));
+      const int rt = (int)(rr / sf.M), n = kv_item_units(sf, ss, rt);
+      long long w0 = sf.off[b] + h * kv_head_units(sf, ss);
+      for (int k = 0; k < rt; ++k) w0 += kv_item_units(sf, ss, k);
+      p[1] = kv_pieces(sf, WS, GS, w0, n, (int)(rr - (long long)rt * sf.M));
       if (p[1].n == 1) p[1].o = sf.row_o, p[1].lse = sf.row_lse, p[1].first = row;
     }
     kv_merge_row<D>(sf, x, p, kKvMergeThreads / 32, sm);

@@ -74,6 +74,11 @@ __device__ __forceinline__ float ld_shared_f(uint32_t addr) {
   return v;
 }
 
+// mbar_wait by a whole warp, with one answer for all lanes: the warp-wide instructions that follow need every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const Abort& ab) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -120,7 +125,9 @@ struct KvNarrowLayout {
   static_assert(kM * kRowPad * 4 <= kRingPad, "a warp's result fits in its ring");
   static constexpr uint32_t kOffMl = 4 * kRingPad;                // [4][kM] m, [4][kM] l, [4] V scale
   static constexpr uint32_t kOffBar = kOffMl + (8 * kM + 4) * 4;
-  static constexpr uint32_t kSmem = kOffBar + 4 * kStages * 8 + 16;
+  static constexpr uint32_t kOffScan = kOffBar + 4 * kStages * 8 + 16;
+  static constexpr uint32_t kSmem = kOffScan + (uint32_t)sizeof(KvScan);
+  static_assert(kOffBar % 8 == 0, "barrier alignment");
   static_assert(kCtasPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
 };
 
@@ -134,7 +141,6 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
   constexpr int M = L::kM, S = L::kStages;
   constexpr int NH = D / 64;   // 64-byte halves of a key row
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ KvScan scan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, c4 = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar) + warp * S;
@@ -157,22 +163,22 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
   }
   int G = gridDim.x, b;
   long long rem;
-  const long long W = kv_place<M, 128>(a, blockIdx.x, G, &scan, &b, &rem, blockIdx.x == 0);
+  const long long W = kv_place<128>(a, blockIdx.x, G, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem, blockIdx.x == 0);
   __syncthreads();
   if (b < 0 || *abort_flag) return;
   const Abort ab{abort_flag, a.err};
   const uint64_t pol = policy_evict_first();
   const long long u0 = kv_cut(W, G, blockIdx.x), u1 = kv_cut(W, G, blockIdx.x + 1);
   KvSeq s = kv_seq(a, b, false);
-  KvPlace at = kv_within<M>(a, s, b, rem);
+  KvPlace at = kv_within(a, s, b, rem);
   const int begin = kv_begin(a);
   uint32_t issued = 0, used = 0;  // slices this warp has asked for and consumed, over all items
   bool ok = true;
 
   for (long long u = u0; u < u1 && ok;) {
-    const int n_item = kv_item_units<M>(a, s, at.rt);
+    const int n_item = kv_item_units(a, s, at.rt);
     const int n = (int)min((long long)(n_item - at.unit), u1 - u);
-    const int item_end = kv_item_end<M>(a, s, at.rt);
+    const int item_end = kv_item_end(a, s, at.rt);
     // this warp's slices: 32 keys at first + 128 j, j < steps
     const int first = begin + at.unit * kKvUnit + warp * 32;
     int steps = n;
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
       uint2 raw[2][NH * 4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const KvRow x = kv_row_of<M>(a, s, at.h, at.rt, mt * 16 + half * 8 + g8);
+        const KvRow x = kv_row_of(a, s, at.h, at.rt, mt * 16 + half * 8 + g8);
         end[mt][half] = x.end;
         if (x.token >= 0) end_min = min(end_min, x.end);
         const long long qo = x.token * a.q_sn + x.head * a.q_sh;
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
 
     for (int j = 0; j < steps; ++j) {
       const int st = used % S;
-      if (!mbar_wait(bars + st, (used / S) & 1u, ab)) {
+      if (!mbar_wait_warp(bars + st, (used / S) & 1u, ab)) {
         ok = false;
         break;
       }
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
 #pragma unroll 1
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 16 + (threadIdx.x >> 3), col0 = (threadIdx.x & 7) * (D / 8);
-      const KvRow x = kv_row_of<M>(a, s, at.h, at.rt, r);
+      const KvRow x = kv_row_of(a, s, at.h, at.rt, r);
       if (x.token >= 0) {
         float mx = -INFINITY, f[4], sum = 0.f;
 #pragma unroll
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     fence_proxy_async_smem();  // the rings are written by TMA again
     __syncthreads();
     u += n;
-    if (u < u1 && !kv_next<M>(a, s, at)) break;
+    if (u < u1 && !kv_next(a, s, at)) break;
   }
   if (!ok) {
     // leave no copy in flight
