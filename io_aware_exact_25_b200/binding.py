@@ -147,9 +147,9 @@ def _open(path: str) -> ctypes.CDLL:
     lib.fa_bwd_dq_accumulator_bytes.restype = SZ
     lib.fa_bwd_recompute_range.argtypes = [vp, vp, vp, vp, vp, vp, I, I, I, I, F, I, F, U64, I, I, vp, SZ, vp]
     KC, I64 = ctypes.POINTER(FaKvCache), ctypes.c_int64
-    lib.fa_kv_append.argtypes = [KC, vp, vp, SP, vp, I, I64, vp, vp, I, I, vp]
-    lib.fa_kv_read.argtypes = [KC, vp, vp, SP, vp, I, I64, vp, vp, I, I, vp]
-    lib.fa_fwd_kvcache.argtypes = [vp, vp, vp, SP, KC, vp, I, I64, vp, vp, I, I, I, I, F, I, I, vp, SZ, vp]
+    lib.fa_kv_append.argtypes = [KC, vp, vp, vp, vp, I, I64, vp, vp, I, I, vp]
+    lib.fa_kv_read.argtypes = [KC, vp, vp, vp, vp, I, I64, vp, vp, I, I, vp]
+    lib.fa_fwd_kvcache.argtypes = [vp, vp, vp, vp, KC, vp, I, I64, vp, vp, I, I, I, I, F, I, I, vp, SZ, vp]
     lib.fa_fwd_kvcache_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.fa_fwd_kvcache_workspace_size.restype = SZ
     lib.fa_strerror.argtypes = [I]
@@ -544,13 +544,17 @@ def bwd_finalize(dq, workspace, scale, stream=None):
     return dq
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _on(device, stream):
-    """(context, stream handle) for a call on tensors of ``device``: its context makes that device and the given
-    stream current, so that what is allocated inside belongs to them; None needs no context."""
+    """(context, stream handle) for a call on tensors of ``device``: inside the context that device and the given
+    stream are current, so that what is allocated there belongs to them."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return None, torch.cuda.current_stream().cuda_stream
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+        index = device.index
+        if index == torch.cuda.current_device():
+            return _NO_CONTEXT, torch._C._cuda_getCurrentRawStream(index)
+        return torch.cuda.device(device), torch._C._cuda_getCurrentRawStream(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
@@ -603,19 +607,29 @@ def _check_table(block_table, device):
 
 
 def _check_tokens(name, t, shape, device):
-    """bf16 [T, H, d] on the cache's device."""
+    """bf16 tensor of the given shape on the cache's device."""
     if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on the cache's device (there is no CPU path)")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be bf16")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _rows_usable(t) -> bool:
     """Rows the kernels can address directly: unit last stride, 16-byte aligned row starts."""
-    return t.stride(-1) == 1 and t.stride(0) >= 0 and t.stride(1) >= 0 and t.stride(0) % 8 == 0 \
-        and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0
+    n, h, c = t.stride()
+    return c == 1 and n >= 0 and h >= 0 and (n | h) & 7 == 0 and t.data_ptr() & 15 == 0
+
+
+_SixInts = ctypes.c_int64 * 6
+
+
+def _pair_strides(a, b):
+    """fa_strides[2] of two token-major tensors, as the six integers they are made of."""
+    a0, a1, _ = a.stride()
+    b0, b1, _ = b.stride()
+    return _SixInts(0, a1, a0, 0, b1, b0)
 
 
 def _kv_rows(fn, what, cache, tensors, k, v, block_table, starts, cu_seqlens, stream):
@@ -629,10 +643,10 @@ def _kv_rows(fn, what, cache, tensors, k, v, block_table, starts, cu_seqlens, st
     elif T != B:
         raise ValueError("without cu_seqlens there is one token per sequence")
     ctx, s = _on(device, stream)
-    with ctx if ctx is not None else contextlib.nullcontext():
+    with ctx:
         if fn.__name__ == "fa_kv_append":  # inputs of other layouts are copied once, on the call's stream
             k, v = (t if _rows_usable(t) else t.contiguous() for t in (k, v))
-        _call(fn(ctypes.byref(cache), _ptr(k), _ptr(v), _tok_strides(k, v), _ptr(block_table), max_pages,
+        _call(fn(ctypes.byref(cache), _ptr(k), _ptr(v), _pair_strides(k, v), _ptr(block_table), max_pages,
                  block_table.stride(0), _ptr(starts), _ptr(cu_seqlens), B, T, s), what)
 
 
@@ -654,7 +668,7 @@ def kv_read(cache, tensors, block_table, total_tokens, starts=None, cu_seqlens=N
     shape = (int(total_tokens), H, d)
     ctx, s = _on(device, stream)
     if k is None or v is None:
-        with ctx if ctx is not None else contextlib.nullcontext():
+        with ctx:
             k = torch.empty(shape, dtype=torch.bfloat16, device=device) if k is None else k
             v = torch.empty(shape, dtype=torch.bfloat16, device=device) if v is None else v
     _check_tokens("k", k, shape, device)
@@ -690,7 +704,7 @@ def fwd_kvcache(q, cache, tensors, block_table, seqlens, max_q, cu_seqlens_q=Non
         scale = 1.0 / math.sqrt(d)
     lib = load()
     ctx, s = _on(device, stream)
-    with ctx if ctx is not None else contextlib.nullcontext():
+    with ctx:
         if not _rows_usable(q):
             q = q.contiguous()
         if o is None:
@@ -706,7 +720,7 @@ def fwd_kvcache(q, cache, tensors, block_table, seqlens, max_q, cu_seqlens_q=Non
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
         elif workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        _call(lib.fa_fwd_kvcache(_ptr(q), _ptr(o), _ptr(lse), _tok_strides(q, o), ctypes.byref(cache),
+        _call(lib.fa_fwd_kvcache(_ptr(q), _ptr(o), _ptr(lse), _pair_strides(q, o), ctypes.byref(cache),
                                  _ptr(block_table), max_pages, block_table.stride(0), _ptr(seqlens),
                                  _ptr(cu_seqlens_q), B, Hq, T, max_q, float(scale), int(bool(causal)), prefix_len,
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), s), "fa_fwd_kvcache")

@@ -160,25 +160,28 @@ Choice choose(long long rows, int d) {
   return {256, kSms};
 }
 
+// Byte offsets in the workspace: the pieces of one launch and the entries that say where they are.
 struct Pieces {
-  size_t o, lse, end;  // byte offsets in the workspace
+  size_t o, lse, cuts, end;
 };
 
-Pieces place_pieces(size_t at, const Choice& c, int d) {
+Pieces place_pieces(size_t at, const Choice& c, int d, size_t entries) {
   Pieces p;
   const size_t rows = 2ull * c.G * c.M;
   p.o = at;
   p.lse = p.o + rows * d * 4;
-  p.end = round_up(p.lse + rows * 4, 256);
+  p.cuts = round_up(p.lse + rows * 4, 256);
+  p.end = round_up(p.cuts + entries * sizeof(fa::KvCut), 256);
   return p;
 }
 
-// Workspace: the pieces of one launch, or, with a shared prefix, the pieces and result rows of both phases and the
-// sequences' places on the suffix's line of work.
+size_t tiles_of(long long rows, const Choice& c) { return (size_t)((rows + c.M - 1) / c.M); }
+
+// Workspace: the pieces of one launch, or, with a shared prefix, the pieces and result rows of both phases.
 struct Layout {
   Choice whole, prefix, suffix;
   Pieces pw, pp, ps;
-  size_t prefix_o, prefix_lse, suffix_o, suffix_lse, off, bytes;
+  size_t prefix_o, prefix_lse, suffix_o, suffix_lse, bytes;
 };
 
 Layout layout_of(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len) {
@@ -187,22 +190,40 @@ Layout layout_of(int B, int Hq, int Hkv, int d, int total_q, int max_q, int pref
   const int g = Hq / Hkv;
   if (prefix_len == 0) {
     l.whole = choose((long long)max_q * g, d);
-    l.pw = place_pieces(0, l.whole, d);
+    l.pw = place_pieces(0, l.whole, d, l.whole.G);
     l.bytes = l.pw.end;
     return l;
   }
   l.prefix = choose((long long)total_q * g, d);
   l.suffix = choose((long long)max_q * g, d);
-  l.pp = place_pieces(0, l.prefix, d);
-  l.ps = place_pieces(l.pp.end, l.suffix, d);
+  l.pp = place_pieces(0, l.prefix, d, Hkv * tiles_of((long long)total_q * g, l.prefix));
+  l.ps = place_pieces(l.pp.end, l.suffix, d, (size_t)B * Hkv * tiles_of((long long)max_q * g, l.suffix));
   const size_t rows = (size_t)total_q * Hq;
   l.prefix_o = l.ps.end;
   l.suffix_o = l.prefix_o + rows * d * 4;
   l.prefix_lse = l.suffix_o + rows * d * 4;
   l.suffix_lse = l.prefix_lse + rows * 4;
-  l.off = round_up(l.suffix_lse + rows * 4, 256);
-  l.bytes = l.off + ((size_t)B + 1) * 8;
+  l.bytes = l.suffix_lse + rows * 4;
   return l;
+}
+
+// Launch on st; `beside` lets the kernel be scheduled while its predecessor still runs (it then waits for the
+// predecessor's completion itself, where it needs it).
+template <class... P, class... A>
+int launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool beside, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = beside ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
 template <int D, int FMT, int MT>
@@ -216,9 +237,7 @@ int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, c
   if ((rc = make_code_map(&mv, c->v, c, box)) != FA_OK) return rc;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
   if (e != cudaSuccess) return fa_host::cuda_fail(e);
-  kern<<<ch.G, 128, L::kSmem, st>>>(mk, mv, a);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+  return launch(kern, dim3(ch.G), 128, L::kSmem, st, a.phase == fa::kKvSuffix, mk, mv, a);
 }
 
 template <int D, int FMT>
@@ -227,9 +246,7 @@ int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
   auto kern = fa::kv_wide_kernel<D, FMT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
   if (e != cudaSuccess) return fa_host::cuda_fail(e);
-  kern<<<ch.G, L::kThreads, L::kSmem, st>>>(a);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+  return launch(kern, dim3(ch.G), L::kThreads, L::kSmem, st, a.phase == fa::kKvSuffix, a);
 }
 
 template <int D, int FMT>
@@ -248,26 +265,21 @@ int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cu
 }
 
 int launch_merge_cut(const fa::KvArgs& a, int d, const Choice& ch, cudaStream_t st) {
-  if (ch.G < 2) return FA_OK;
-  // Few items: a block for each row of a cut item, which may be in many pieces.  Many items: few blocks a cut, each
-  // walking the item's rows, so that the blocks that find nothing to do stay few.
-  const long long items = (long long)a.B * a.Hkv * (((long long)a.max_q * a.g + ch.M - 1) / ch.M);
-  const unsigned y = items <= 64 ? (ch.M < 64 ? ch.M : 64) : (ch.M + 31) / 32;
-  const dim3 grid((unsigned)(ch.G - 1), y);
-  if (d == 64) fa::kv_merge_cut_kernel<64><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
-  else fa::kv_merge_cut_kernel<128><<<grid, fa::kKvMergeThreads, 0, st>>>(a, ch.G);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+  // Few items: a block for each row of a cut item, which may be in many pieces.  Many items: a block per eight rows.
+  const long long items = (long long)a.B * a.Hkv * tiles_of((long long)a.max_q * a.g, ch);
+  const dim3 grid((unsigned)ch.G, (unsigned)(items <= 64 && ch.M < 64 ? ch.M : ch.M / 8));
+  return d == 64 ? launch(fa::kv_merge_cut_kernel<64>, grid, fa::kKvMergeThreads, 0, st, true, a)
+                 : launch(fa::kv_merge_cut_kernel<128>, grid, fa::kKvMergeThreads, 0, st, true, a);
 }
 
-int launch_merge_prefix(const fa::KvArgs& pf, const fa::KvArgs& sf, int d, const Choice& cp, const Choice& cs,
-                        cudaStream_t st) {
-  const long long rows = (long long)sf.total * sf.Hq;
-  const unsigned grid = (unsigned)(rows < kSms * 64 ? rows : kSms * 64);
-  if (d == 64) fa::kv_merge_prefix_kernel<64><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
-  else fa::kv_merge_prefix_kernel<128><<<grid, fa::kKvMergeThreads, 0, st>>>(pf, sf, cp.G, cs.G);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
+int launch_merge_prefix(const fa::KvArgs& pf, const fa::KvArgs& sf, int d, const Choice& cp, cudaStream_t st) {
+  // a prefix of few items is in many pieces a row: then a block merges one row
+  const size_t items = pf.Hkv * tiles_of((long long)pf.total * pf.g, cp);
+  const int group = (size_t)cp.G > 8 * items ? fa::kKvMergeThreads / 32 : 1;
+  const size_t per = fa::kKvMergeThreads / 32 / group, rows = (size_t)sf.total * sf.Hq;
+  const dim3 grid((unsigned)((rows + per - 1) / per));
+  return d == 64 ? launch(fa::kv_merge_prefix_kernel<64>, grid, fa::kKvMergeThreads, 0, st, true, pf, sf, group)
+                 : launch(fa::kv_merge_prefix_kernel<128>, grid, fa::kKvMergeThreads, 0, st, true, pf, sf, group);
 }
 
 // Checks of sizes that fa_fwd_kvcache and its workspace size share: FA_OK, a negative status, or 1 for nothing to do.
@@ -277,6 +289,7 @@ int check_attend(int B, int Hq, int Hkv, int d, int total_q, int max_q, int pref
   if (B == 0 || Hq == 0 || total_q == 0 || max_q == 0) return 1;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (Hq > (1 << 16) || B > (1 << 24) || total_q > (1 << 24) || max_q > (1 << 24)) return FA_ERR_TOO_LARGE;
+  if ((long long)total_q * Hq > 0x7fff0000ll) return FA_ERR_TOO_LARGE;  // row numbers are 32-bit
   return FA_OK;
 }
 
@@ -308,7 +321,7 @@ int fa_kv_read(const fa_kv_cache* cache, void* k, void* v, const fa_strides* str
 
 size_t fa_fwd_kvcache_workspace_size(int B, int Hq, int Hkv, int d, int total_q, int max_q, int prefix_len) {
   if (check_attend(B, Hq, Hkv, d, total_q, max_q, prefix_len) != FA_OK) return 0;
-  return layout_of(B, Hq, Hkv, d, total_q, max_q, B > 1 ? prefix_len : 0).bytes;
+  return layout_of(B, Hq, Hkv, d, total_q, max_q < total_q ? max_q : total_q, B > 1 ? prefix_len : 0).bytes;
 }
 
 int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides, const fa_kv_cache* cache,
@@ -331,6 +344,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
     return FA_ERR_ALIGNMENT;
   if (!tok_strides_ok(strides[0]) || !tok_strides_ok(strides[1])) return FA_ERR_ALIGNMENT;
   if (B == 1) prefix_len = 0;  // nothing is shared
+  if (max_q > total_q) max_q = total_q;
   const Layout l = layout_of(B, Hq, Hkv, d, total_q, max_q, prefix_len);
   if (!workspace || workspace_bytes < l.bytes) return FA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return FA_ERR_ALIGNMENT;
@@ -364,28 +378,33 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   if (prefix_len == 0) {
     a.phase = fa::kKvWhole;
     a.M = l.whole.M;
+    a.G = l.whole.G;
     a.part_o = reinterpret_cast<float*>(ws + l.pw.o);
     a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
+    a.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pw.cuts);
     if ((rc = launch_phase(cache, a, l.whole, st)) != FA_OK) return rc;
     return launch_merge_cut(a, d, l.whole, st);
   }
   fa::KvArgs pf = a, sf = a;
   pf.phase = fa::kKvPrefix;
   pf.M = l.prefix.M;
+  pf.G = l.prefix.G;
   pf.part_o = reinterpret_cast<float*>(ws + l.pp.o);
   pf.part_lse = reinterpret_cast<float*>(ws + l.pp.lse);
+  pf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pp.cuts);
   pf.row_o = reinterpret_cast<float*>(ws + l.prefix_o);
   pf.row_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
   sf.phase = fa::kKvSuffix;
   sf.M = l.suffix.M;
+  sf.G = l.suffix.G;
   sf.part_o = reinterpret_cast<float*>(ws + l.ps.o);
   sf.part_lse = reinterpret_cast<float*>(ws + l.ps.lse);
+  sf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.ps.cuts);
   sf.row_o = reinterpret_cast<float*>(ws + l.suffix_o);
   sf.row_lse = reinterpret_cast<float*>(ws + l.suffix_lse);
-  sf.off = reinterpret_cast<long long*>(ws + l.off);
   if ((rc = launch_phase(cache, pf, l.prefix, st)) != FA_OK) return rc;
   if ((rc = launch_phase(cache, sf, l.suffix, st)) != FA_OK) return rc;
-  return launch_merge_prefix(pf, sf, d, l.prefix, l.suffix, st);
+  return launch_merge_prefix(pf, sf, d, l.prefix, st);
 }
 
 }  // extern "C"

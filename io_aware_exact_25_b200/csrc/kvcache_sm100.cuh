@@ -46,7 +46,7 @@ struct KvArgs {
   int max_q;   // largest number of query rows of a sequence
   int causal;
   float scale_log2;  // scale * log2(e)
-  int M;             // rows of an item tile
+  int M, G;          // rows of an item tile; CTAs of the launch
   int prefix_len;    // keys [0, prefix_len) are the batch's shared prefix (0: none)
   int phase;         // kKvWhole: all keys; kKvPrefix: the shared ones; kKvSuffix: the rest
   // pieces of items that several CTAs share: slot 2 c + s of CTA c
@@ -55,7 +55,14 @@ struct KvArgs {
   // whole results of a phase, merged afterwards (phases other than kKvWhole)
   float* row_o;      // [total * Hq][D], normalised
   float* row_lse;    // [total * Hq], base 2
-  long long* off;    // [B + 1] work units before each sequence
+  struct KvCut* cuts;  // where the pieces are: one entry per CTA (kKvWhole) or per item (else)
+};
+
+// An item's pieces: `first`, then every second one from `next` on, n in all.  kKvWhole: the entry of CTA c is the
+// item that c starts and does not finish (n = 0: none).  Other phases: the entry of an item; n = 1 is a finished item,
+// whose rows are in row_o and row_lse.
+struct KvCut {
+  int n, first, next, b, h, rt, pad[2];
 };
 
 enum : int { kKvWhole = 0, kKvPrefix = 1, kKvSuffix = 2 };
@@ -89,18 +96,35 @@ __device__ __forceinline__ long long kv_row(const KvArgs& a, int b, long long po
   return (((long long)page * a.Hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
+// x / y for x >= 0, y > 0; almost always of 32-bit numbers, whose division is several times shorter.
+__device__ __forceinline__ long long kv_div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (long long)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
+
+// Programmatic dependent launch: allow the next kernel of the stream to be scheduled, and wait for the previous one's
+// completion (both do nothing in launches without the attribute).
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // --------------------------------------------------------------- rounding
 
 // y rounded to 20 significant bits.  The exact quotient top * x / amax of bf16
 // numbers is either on a border between two codes (a dyadic number of few
 // bits) or further than 2^-16 of its value away from one: with 8-bit integers
 // X, A and a border of M / 2^n, M < 2^8, |top X 2^i - M A| is a whole number of
-// units of which M A is at most 2^16.  y carries a relative error of 2^-23 (a
-// rounded reciprocal, a rounded product), so this rounding puts every border
+// units of which M A is at most 2^16.  y carries a relative error below 2^-21 (a
+// reciprocal good to an ulp, two rounded products), so this rounding puts every border
 // case exactly on its border and moves nothing across one: the code that
 // follows is the exact quotient's, half to even, without a division.
 __device__ __forceinline__ float kv_snap(float y) {
   return __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int FMT>
@@ -195,16 +219,28 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
     for (int s = 1; s < LPR; s <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, s));
     const uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
     const float amax = __uint_as_float(mb << 16);
-    // tiny rows are lifted by 2^100 so that the reciprocal stays in range
-    const float lift = amax < 7.888609052210118e-31f ? 1.2676506002282294e30f : 1.f;
     const bool finite = mb < 0x7f80u;
-    const float inv = finite && mb != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
+    // top / amax to an ulp or two (the codes ask for no more), and amax / top by one step of Newton's division on
+    // the rounded reciprocal of top: the residual fma is exact, so the quotient is correctly rounded
+    float lift = 1.f, inv = kTop * rcp_approx(amax);
+    const float s0 = amax * (1.f / kTop);
+    float scale = fmaf(fmaf(-kTop, s0, amax), 1.f / kTop, s0);
+    const bool tiny = amax < 7.888609052210118e-31f;  // below 2^-100: lifted by 2^100, so that nothing leaves the range
+    if (tiny) {
+      lift = 1.2676506002282294e30f;
+      inv = mb != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
+      scale = __fdiv_rn(amax, kTop);
+    }
+    const bool any_tiny = __any_sync(0xffffffffu, tiny);
     uint32_t c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float y[4] = {bf16_lo(xs[2 * i]), bf16_hi(xs[2 * i]), bf16_lo(xs[2 * i + 1]), bf16_hi(xs[2 * i + 1])};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = finite ? y[e] * lift * inv : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        if (any_tiny) y[e] *= lift;
+        y[e] = finite ? y[e] * inv : 0.f;
+      }
       c[i] = kv_encode4<FMT>(y[0], y[1], y[2], y[3]);
     }
     if (r < 2 * a.Hkv) {
@@ -215,7 +251,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
       if (FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
         *reinterpret_cast<uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col) = make_uint2(c[0], c[1]);
         if (lane % LPR == 0)
-          (r < a.Hkv ? a.ks : a.vs)[at] = finite ? __fdiv_rn(amax, kTop) : __uint_as_float(0x7fc00000u);
+          (r < a.Hkv ? a.ks : a.vs)[at] = finite ? scale : __uint_as_float(0x7fc00000u);
       }
     }
   }
@@ -318,12 +354,13 @@ __device__ __forceinline__ int kv_begin(const KvArgs& a) { return a.phase == kKv
 
 // one past the last key that some row of tile rt sees
 __device__ __forceinline__ int kv_item_end(const KvArgs& a, const KvSeq& s, int rt) {
-  const long long last = min((long long)(rt + 1) * a.M, (long long)s.lq * a.g) - 1;
-  return kv_end(a, s, (int)(last / a.g));
+  // rows of a call are fewer than 2^31, so row numbers stay 32-bit
+  const uint32_t last = min((uint32_t)(rt + 1) * (uint32_t)a.M, (uint32_t)s.lq * (uint32_t)a.g) - 1u;
+  return kv_end(a, s, (int)(last / (uint32_t)a.g));
 }
 
 __device__ __forceinline__ int kv_tiles(const KvArgs& a, const KvSeq& s) {
-  return (int)(((long long)s.lq * a.g + a.M - 1) / a.M);
+  return (int)(((uint32_t)s.lq * (uint32_t)a.g + (uint32_t)a.M - 1u) / (uint32_t)a.M);
 }
 
 __device__ __forceinline__ int kv_item_units(const KvArgs& a, const KvSeq& s, int rt) {
@@ -343,10 +380,17 @@ __device__ __forceinline__ long long kv_head_units(const KvArgs& a, const KvSeq&
 
 __device__ __forceinline__ int kv_num_seqs(const KvArgs& a) { return a.phase == kKvPrefix ? 1 : a.B; }
 
-// First unit of CTA c's stretch, and the CTA whose stretch holds unit u.  G is the number of stretches: the grid,
-// or one per unit where there are fewer units than CTAs, so none is empty.
-__device__ __forceinline__ long long kv_cut(long long W, int G, int c) { return W * c / G; }
-__device__ __forceinline__ int kv_cta_of(long long W, int G, long long u) { return (int)(((u + 1) * G - 1) / W); }
+// The line of W units in G stretches -- one per CTA of the grid, or one per unit where there are fewer units than
+// CTAs, so that none is empty: the first r stretches have q + 1 units, the others q.
+struct KvLine {
+  long long q;
+  int r, G;
+  __device__ __forceinline__ long long cut(int c) const { return q * c + min(c, r); }  // first unit of stretch c
+  __device__ __forceinline__ int cta_of(long long u) const {                           // stretch that holds unit u
+    const long long wide = (q + 1) * r;
+    return u < wide ? (int)kv_div(u, q + 1) : r + (int)kv_div(u - wide, q);
+  }
+};
 
 // A place on the line of units: unit `unit` of row tile rt of head h of sequence b.
 struct KvPlace {
@@ -382,62 +426,50 @@ __device__ __forceinline__ long long kv_block_inclusive(long long x, KvScan* sc,
   return before + x;
 }
 
-// The line's length W, and the sequence that holds the first unit of CTA c (and the units before it within the
-// sequence), by the whole block.  Returns W and clamps G to the stretches there are; *b < 0 if CTA c has none.
-// In the suffix phase CTA 0 also records every sequence's first unit.
+// The line of work, and the sequence that holds the first unit of CTA c (and the units before it within the
+// sequence), by the whole block; *b < 0 if CTA c has no stretch.
 template <int NT>
-__device__ __forceinline__ long long kv_place(const KvArgs& a, int c, int& G, KvScan* sc, int* b, long long* rem,
-                                              bool report) {
+__device__ __forceinline__ KvLine kv_place(const KvArgs& a, int c, int G, KvScan* sc, int* b, long long* rem) {
   const int n = kv_num_seqs(a);
-  auto units_of = [&](int i, bool rep) -> long long {
+  auto units_of = [&](int i, bool report) -> long long {
     if (i >= n) return 0;
-    const KvSeq s = kv_seq(a, i, rep);
+    const KvSeq s = kv_seq(a, i, report);
     return kv_head_units(a, s) * a.Hkv;
   };
-  long long* off = c == 0 && a.off && a.phase == kKvSuffix ? a.off : nullptr;
-  const long long mine = units_of((int)threadIdx.x, report);  // the first NT sequences' units stay in registers
-  long long W = 0, part = 0;
-  long long first_incl = kv_block_inclusive<NT>(mine, sc, &part);
-  W = part;
+  const long long mine = units_of((int)threadIdx.x, c == 0);  // the first NT sequences' units stay in registers
+  long long part = 0, incl = kv_block_inclusive<NT>(mine, sc, &part);
+  long long W = part;
   if (n > NT) {
-    long long sum = 0;
-    for (int i = NT + threadIdx.x; i < n; i += NT) sum += units_of(i, report);
-    long long rest;
+    long long sum = 0, rest;
+    for (int i = NT + threadIdx.x; i < n; i += NT) sum += units_of(i, c == 0);
     (void)kv_block_inclusive<NT>(sum, sc, &rest);
     W += rest;
   }
-  G = (int)min((long long)G, W);
-  const long long u0 = c < G ? kv_cut(W, G, c) : W;
+  KvLine line{0, 0, (int)min((long long)G, W)};
   *b = -1;
   *rem = 0;
-  if (c >= G && !off) return W;
-  __syncthreads();
-  long long run = 0;
-  bool found = false;
-  for (int base = 0; base < n; base += NT) {
-    const int i = base + threadIdx.x;
-    long long x = mine, incl = first_incl, tot = part;
-    if (base > 0) {
-      x = units_of(i, false);
-      incl = kv_block_inclusive<NT>(x, sc, &tot);
-    }
-    if (off && i < n) off[i] = run + incl - x;
+  if (W == 0) return line;
+  line.q = kv_div(W, line.G);
+  line.r = (int)(W - line.q * line.G);
+  if (c >= line.G) return line;
+  const long long u0 = line.cut(c);
+  long long run = 0, x = mine, tot = part;
+  for (int base = 0;;) {
     const long long lo = run + incl - x;
-    if (!found && u0 >= lo && u0 < lo + x) {
-      sc->place[0] = i;
+    if (u0 >= lo && u0 < lo + x) {
+      sc->place[0] = base + threadIdx.x;
       sc->place[1] = u0 - lo;
     }
-    if (!found && u0 < run + tot) {
-      found = true;
-      __syncthreads();
-      *b = (int)sc->place[0];
-      *rem = sc->place[1];
-      if (!off) break;
-    }
+    if (u0 < run + tot) break;
     run += tot;
+    base += NT;
+    x = units_of(base + threadIdx.x, false);
+    incl = kv_block_inclusive<NT>(x, sc, &tot);
   }
-  if (off && threadIdx.x == 0) off[n] = W;
-  return W;
+  __syncthreads();
+  *b = (int)sc->place[0];
+  *rem = sc->place[1];
+  return line;
 }
 
 // The place `rem` units into sequence b.
@@ -445,13 +477,13 @@ __device__ __forceinline__ KvPlace kv_within(const KvArgs& a, const KvSeq& s, in
   KvPlace p;
   p.b = b;
   const long long per = kv_head_units(a, s);
-  p.h = (int)(rem / per);
+  p.h = (int)kv_div(rem, per);
   rem -= p.h * per;
   p.rt = 0;
   const int nt = kv_tiles(a, s);
   if (nt > 1 && (!a.causal || a.phase == kKvPrefix)) {
     const int n = kv_item_units(a, s, 0);
-    p.rt = (int)(rem / n);
+    p.rt = (int)kv_div(rem, n);
     rem -= (long long)p.rt * n;
   } else {
     for (; p.rt + 1 < nt; ++p.rt) {
@@ -479,6 +511,25 @@ __device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
   return false;
 }
 
+// Entry of the item at p (of n units, the first of them unit u, in CTA c's stretch) in the phases other than kKvWhole.
+__device__ __forceinline__ long long kv_item_index(const KvArgs& a, int b, int h, int rt) {
+  const uint32_t rows = (uint32_t)(a.phase == kKvPrefix ? a.total : a.max_q) * (uint32_t)a.g;
+  const uint32_t tiles = (rows + (uint32_t)a.M - 1u) / (uint32_t)a.M;  // of the longest sequence
+  return ((long long)b * a.Hkv + h) * tiles + rt;
+}
+
+// Record where the item's pieces are; called by one thread of the CTA that starts the item.
+__device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvPlace& p, int c, long long u,
+                                          int n_item, bool whole, bool first_item) {
+  if (whole && a.phase == kKvWhole) return;
+  KvCut k;
+  k.n = whole ? 1 : line.cta_of(u + n_item - 1) - c + 1;
+  k.first = 2 * c + (first_item ? 0 : 1);
+  k.next = 2 * c + 2;
+  k.b = p.b, k.h = p.h, k.rt = p.rt;
+  a.cuts[a.phase == kKvWhole ? c : kv_item_index(a, p.b, p.h, p.rt)] = k;
+}
+
 // Where a row of an item lives: token, query head, and how many keys it sees.
 struct KvRow {
   int token, head, end;
@@ -486,11 +537,11 @@ struct KvRow {
 
 __device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
   KvRow x;
-  const long long rr = (long long)rt * a.M + r;
-  if (rr >= (long long)s.lq * a.g) return KvRow{-1, 0, 0};
-  const int i = (int)(rr / a.g);
+  const uint32_t rr = (uint32_t)rt * (uint32_t)a.M + (uint32_t)r;
+  if (rr >= (uint32_t)s.lq * (uint32_t)a.g) return KvRow{-1, 0, 0};
+  const int i = (int)(rr / (uint32_t)a.g);
   x.token = s.row0 + i;
-  x.head = h * a.g + (int)(rr - (long long)i * a.g);
+  x.head = h * a.g + (int)(rr - (uint32_t)i * (uint32_t)a.g);
   x.end = kv_end(a, s, i);
   if (a.phase == kKvPrefix) {
     // the token's own sequence bounds what it sees of the prefix
@@ -584,62 +635,57 @@ __device__ __forceinline__ float kv_weight(float lse2, float mx) {
   return lse2 == -INFINITY ? 0.f : exp2f(lse2 - mx);
 }
 
-// A piece list of one row: base points at the row in the piece of CTA c0 (slot slot0), the next CTAs' first slots
-// follow.  A finished row of a phase is a list of one.
+// The rows of one row of an item in its pieces (or its finished row): row `first`, then n - 1 rows from `next`,
+// `stride` apart.
 struct KvPieces {
   const float* o;
   const float* lse;
   int n;
-  long long first;   // row of the first piece
-  long long second;  // row of the second piece; the others follow `stride` rows apart
-  long long stride;
-  __device__ __forceinline__ long long at(int k) const { return k == 0 ? first : second + (k - 1) * stride; }
+  long long first, next, stride;
+  __device__ __forceinline__ long long at(int k) const { return k == 0 ? first : next + (k - 1) * stride; }
 };
 
-// The pieces of row r of the item of n units that starts at unit w0.
-__device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, long long W, int G, long long w0, int n, int r) {
-  const int c0 = kv_cta_of(W, G, w0), c1 = kv_cta_of(W, G, w0 + n - 1);
-  const int slot0 = w0 > kv_cut(W, G, c0) ? 1 : 0;
-  KvPieces p;
-  p.o = a.part_o;
-  p.lse = a.part_lse;
-  p.n = c1 - c0 + 1;
-  p.first = (2ll * c0 + slot0) * a.M + r;
-  p.second = (2ll * c0 + 2) * a.M + r;
-  p.stride = 2ll * a.M;
-  return p;
+__device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, const KvCut& k, int r) {
+  return KvPieces{a.part_o, a.part_lse, k.n, (long long)k.first * a.M + r, (long long)k.next * a.M + r, 2ll * a.M};
 }
 
-// Merge of up to two piece lists into row x by `group` warps (1, or all NW of the block; then every warp of the
-// block calls it for the same row):
-//   lse = log2 sum_s 2^lse_s,  O = sum_s 2^(lse_s - lse) O_s
-template <int NW, int D>
-struct KvMergeSmem {
-  float mx[NW], sum[NW], o[NW][D];
-};
+// An entry that can be followed.  Every entry is written by the launch before, unless a wait of it ran out: then the
+// workspace's old contents must not lead anywhere.
+__device__ __forceinline__ bool kv_cut_ok(const KvArgs& a, const KvCut& k) {
+  if (k.n < 1 || k.n > a.G || k.first < 0 || k.first >= 2 * a.G) return false;
+  return k.n == 1 || (k.next >= 0 && (long long)k.next + 2ll * (k.n - 2) < 2ll * a.G);
+}
 
 template <int D>
-__device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces (&p)[2], int group,
-                             KvMergeSmem<kKvMergeThreads / 32, D>& sm) {
+struct KvMergeSmem {
+  float sum[kKvMergeThreads / 32], o[kKvMergeThreads / 32][D];
+};
+
+// Merge of the pieces in up to two lists into row x by `group` warps: one, or all of the block (which then all call it
+// for the same row):
+//   lse = log2 sum_s 2^lse_s,  O = sum_s 2^(lse_s - lse) O_s
+template <int D>
+__device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces& p0, const KvPieces& p1, int group,
+                             KvMergeSmem<D>& sm) {
   constexpr int NW = kKvMergeThreads / 32, PER = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int me = group == 1 ? 0 : warp;
-  float mx = -INFINITY;
-#pragma unroll
-  for (int l = 0; l < 2; ++l)
-    for (int k = lane; k < p[l].n; k += 32) mx = fmaxf(mx, p[l].lse[p[l].at(k)]);
+  const int n = p0.n + p1.n;
+  auto lse_of = [&](int k) { return k < p0.n ? p0.lse[p0.at(k)] : p1.lse[p1.at(k - p0.n)]; };
+  // up to 32 logsumexps in the lanes at once
+  float mx = -INFINITY, held = lane < n ? lse_of(lane) : -INFINITY;
+  mx = held;
+  for (int k = 32 + lane; k < n; k += 32) mx = fmaxf(mx, lse_of(k));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float acc[PER] = {}, sum = 0.f;
-#pragma unroll
-  for (int l = 0; l < 2; ++l) {
 #pragma unroll 4
-    for (int k = me; k < p[l].n; k += group) {
-      const long long at = p[l].at(k);
-      const float wt = kv_weight(p[l].lse[at], mx);
-      sum += wt;
-      kv_axpy<D>(acc, wt, p[l].o + at * D + lane * PER);
-    }
+  for (int k = me; k < n; k += group) {
+    const float ls = k < 32 ? __shfl_sync(0xffffffffu, held, k) : lse_of(k);
+    const float* src = k < p0.n ? p0.o + p0.at(k) * D : p1.o + p1.at(k - p0.n) * D;
+    const float wt = kv_weight(ls, mx);
+    sum += wt;
+    kv_axpy<D>(acc, wt, src + lane * PER);
   }
   if (group > 1) {
 #pragma unroll
@@ -667,81 +713,59 @@ __device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces (&p
   if (group > 1) __syncthreads();
 }
 
-// Items that the stretches cut.  Block (c, y) looks at the cut before CTA
-// c + 1; if that is the first cut inside an item, the blocks of that c merge
-// the item's rows, a warp a row, or with more than eight pieces the block a
-// row with the pieces spread over its warps (one key head's 64K keys leave
-// over a hundred pieces, a chain that one warp would walk alone).
+// Items that the stretches cut.  The blocks (c, .) merge the item that CTA c
+// started and left unfinished: a warp a row, or with more than eight pieces
+// the block a row with the pieces spread over its warps (one key head's 64K
+// keys leave over a hundred pieces, a chain that one warp would walk alone).
 template <int D>
-__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvArgs a, int G) {
+__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvArgs a) {
   constexpr int NW = kKvMergeThreads / 32;
-  __shared__ KvScan sc;
-  __shared__ KvMergeSmem<NW, D> sm;
+  __shared__ KvMergeSmem<D> sm;
   const int warp = threadIdx.x >> 5;
-  const int c = (int)blockIdx.x + 1;
-  int b;
-  long long rem;
-  const long long W = kv_place<kKvMergeThreads>(a, c, G, &sc, &b, &rem, false);
-  if (b < 0) return;
-  const KvSeq s = kv_seq(a, b, false);
-  const KvPlace at = kv_within(a, s, b, rem);
-  if (at.unit == 0) return;  // the cut falls between two items
-  const long long w0 = kv_cut(W, G, c) - at.unit;
-  if (kv_cta_of(W, G, w0) != c - 1) return;  // not the item's first cut
-  const int n = kv_item_units(a, s, at.rt);
-  const int group = kv_pieces(a, W, G, w0, n, 0).n > NW ? NW : 1;
+  pdl_wait();
+  const KvCut k = a.cuts[blockIdx.x];
+  if (k.n == 0) return;
+  const KvSeq s = kv_seq(a, k.b, false);
+  const int group = k.n > NW ? NW : 1;
   const int rows = group == 1 ? NW : 1;  // rows a block merges at a time
   for (int r0 = blockIdx.y * rows; r0 < a.M; r0 += gridDim.y * rows) {
     const int r = r0 + (group == 1 ? warp : 0);
-    const KvRow x = kv_row_of(a, s, at.h, at.rt, r);
+    const KvRow x = kv_row_of(a, s, k.h, k.rt, r);
     if (r >= a.M || x.token < 0) continue;
-    KvPieces p[2];
-    p[0] = kv_pieces(a, W, G, w0, n, r);
-    p[1] = p[0];
-    p[1].n = 0;
-    kv_merge_row<D>(a, x, p, group, sm);
+    KvPieces p = kv_pieces(a, k, r), none = p;
+    none.n = 0;
+    kv_merge_row<D>(a, x, p, none, group, sm);
   }
 }
 
 // Shared prefix: every row's result over the prefix (pf: phase kKvPrefix) and over its own keys (sf: kKvSuffix),
-// each finished or in pieces.  One block a row.
+// each finished or in pieces; `group` warps a row.
 template <int D>
-__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const KvArgs pf, const KvArgs sf, int GP,
-                                                                          int GS) {
-  __shared__ KvMergeSmem<kKvMergeThreads / 32, D> sm;
-  const int lane = threadIdx.x & 31;
-  const KvSeq ps = kv_seq(pf, 0, false);
-  const long long WP = kv_head_units(pf, ps) * pf.Hkv;
-  const long long WS = sf.off[sf.B];
-  GP = (int)min((long long)GP, WP);
-  GS = (int)min((long long)GS, WS);
-  const long long rows = (long long)sf.total * sf.Hq;
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int t = (int)(row / sf.Hq), head = (int)(row - (long long)t * sf.Hq);
-    const int h = head / sf.g;
-    int b = sf.cu ? kv_find_seq(sf.cu, sf.B, t, lane) : t / sf.max_q;
-    const KvSeq ss = kv_seq(sf, b, false);
-    const int i = t - ss.row0;
-    if (i < 0 || i >= ss.lq) continue;  // a row of no sequence
-    const KvRow x{t, head, 0};
-    KvPieces p[2];
-    {
-      const long long rr = (long long)t * pf.g + (head - h * pf.g);
-      const int rt = (int)(rr / pf.M), n = kv_item_units(pf, ps, rt);
-      const long long w0 = ((long long)h * kv_tiles(pf, ps) + rt) * n;
-      p[0] = kv_pieces(pf, WP, GP, w0, n, (int)(rr - (long long)rt * pf.M));
-      if (p[0].n == 1) p[0].o = pf.row_o, p[0].lse = pf.row_lse, p[0].first = row;
-    }
-    {
-      const long long rr = (long long)i * sf.g + (head - h * sf.g);
-      const int rt = (int)(rr / sf.M), n = kv_item_units(sf, ss, rt);
-      long long w0 = sf.off[b] + h * kv_head_units(sf, ss);
-      for (int k = 0; k < rt; ++k) w0 += kv_item_units(sf, ss, k);
-      p[1] = kv_pieces(sf, WS, GS, w0, n, (int)(rr - (long long)rt * sf.M));
-      if (p[1].n == 1) p[1].o = sf.row_o, p[1].lse = sf.row_lse, p[1].first = row;
-    }
-    kv_merge_row<D>(sf, x, p, kKvMergeThreads / 32, sm);
-  }
+__global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const KvArgs pf, const KvArgs sf, int group) {
+  constexpr int NW = kKvMergeThreads / 32;
+  __shared__ KvMergeSmem<D> sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = NW / group;  // rows a block merges at a time
+  const uint32_t rows = (uint32_t)sf.total * (uint32_t)sf.Hq;
+  const uint32_t row = blockIdx.x * (uint32_t)per + (group == 1 ? warp : 0);
+  if (row >= rows) return;  // (one warp, or the whole block)
+  const int t = (int)(row / (uint32_t)sf.Hq), head = (int)(row - (uint32_t)t * (uint32_t)sf.Hq);
+  const int h = head / sf.g;
+  const int b = sf.cu ? kv_find_seq(sf.cu, sf.B, t, lane) : t / sf.max_q;
+  const KvSeq ss = kv_seq(sf, b, false);
+  const int i = t - ss.row0;
+  const uint32_t rp = (uint32_t)t * (uint32_t)pf.g + (uint32_t)(head - h * pf.g);
+  const uint32_t rs = (uint32_t)max(i, 0) * (uint32_t)sf.g + (uint32_t)(head - h * sf.g);
+  const uint32_t tp = rp / (uint32_t)pf.M, ts = rs / (uint32_t)sf.M;
+  pdl_wait();
+  if (i < 0 || i >= ss.lq) return;  // a row of no sequence
+  const KvCut kp = pf.cuts[kv_item_index(pf, 0, h, (int)tp)], ks = sf.cuts[kv_item_index(sf, b, h, (int)ts)];
+  if (!kv_cut_ok(pf, kp) || !kv_cut_ok(sf, ks)) return;
+  KvPieces p0 = kv_pieces(pf, kp, (int)(rp - tp * (uint32_t)pf.M));
+  KvPieces p1 = kv_pieces(sf, ks, (int)(rs - ts * (uint32_t)sf.M));
+  if (kp.n == 1) p0.o = pf.row_o, p0.lse = pf.row_lse, p0.first = row;
+  if (ks.n == 1) p1.o = sf.row_o, p1.lse = sf.row_lse, p1.first = row;
+  kv_merge_row<D>(sf, KvRow{t, head, 0}, p0, p1, group, sm);
 }
 
 }  // namespace fa

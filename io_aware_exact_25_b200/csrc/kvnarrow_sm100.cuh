@@ -161,14 +161,20 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  int G = gridDim.x, b;
+  pdl_trigger();
+  int b;
   long long rem;
-  const long long W = kv_place<128>(a, blockIdx.x, G, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem, blockIdx.x == 0);
+  const KvLine line =
+      kv_place<128>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem);
   __syncthreads();
-  if (b < 0 || *abort_flag) return;
+  if (a.phase == kKvWhole && threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;  // until this CTA leaves an item unfinished
+  if (b < 0 || *abort_flag) {
+    if (a.phase == kKvSuffix) pdl_wait();
+    return;
+  }
   const Abort ab{abort_flag, a.err};
   const uint64_t pol = policy_evict_first();
-  const long long u0 = kv_cut(W, G, blockIdx.x), u1 = kv_cut(W, G, blockIdx.x + 1);
+  const long long u0 = line.cut(blockIdx.x), u1 = line.cut(blockIdx.x + 1);
   KvSeq s = kv_seq(a, b, false);
   KvPlace at = kv_within(a, s, b, rem);
   const int begin = kv_begin(a);
@@ -467,6 +473,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     // each row by 128 / 16 = 8 threads, D / 8 columns each
     const bool whole = at.unit == 0 && n == n_item;
     const int slot = u == u0 ? 0 : 1;
+    if (at.unit == 0 && threadIdx.x == 0) kv_record(a, line, at, blockIdx.x, u, n_item, whole, u == u0);
 #pragma unroll 1
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 16 + (threadIdx.x >> 3), col0 = (threadIdx.x & 7) * (D / 8);
@@ -508,6 +515,8 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     // leave no copy in flight
     for (uint32_t i = used; i < issued; ++i) mbar_wait_drain(bars + i % S, (i / S) & 1u);
   }
+  // the suffix may run beside the prefix; its completion, which the merge waits for, has to mean both
+  if (a.phase == kKvSuffix) pdl_wait();
 }
 
 }  // namespace fa

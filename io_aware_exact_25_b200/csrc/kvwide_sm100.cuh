@@ -111,16 +111,19 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  int G = gridDim.x, b;
+  pdl_trigger();
+  int b;
   long long rem;
-  const long long W = kv_place<512>(a, blockIdx.x, G, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem, blockIdx.x == 0);
+  const KvLine line =
+      kv_place<512>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Abort ab{abort_flag, a.err};
   const bool run = b >= 0 && *abort_flag == 0;
-  const long long u0 = b >= 0 ? kv_cut(W, G, blockIdx.x) : 0, u1 = b >= 0 ? kv_cut(W, G, blockIdx.x + 1) : 0;
+  if (a.phase == kKvWhole && threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;  // until this CTA leaves an item unfinished
+  const long long u0 = b >= 0 ? line.cut(blockIdx.x) : 0, u1 = b >= 0 ? line.cut(blockIdx.x + 1) : 0;
   const int begin = kv_begin(a);
   KvSeq s{0, 0, 0};
   KvPlace at{0, 0, 0, 0};
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
   }
   // Every role walks the same items: n units of the item at `at`, from key `first` on; act1 if the second row tile
   // has rows.
-  auto act1_of = [&]() { return (long long)at.rt * 256 + 128 < (long long)s.lq * a.g; };
+  auto act1_of = [&]() { return (uint32_t)at.rt * 256u + 128u < (uint32_t)s.lq * (uint32_t)a.g; };
 
   if (warp >= 12) {
     regs_dec<L::kRegsCtl>();
@@ -511,6 +514,7 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
           if (ok) {
             tc_fence_after();
             const bool whole = at.unit == 0 && n == n_item;
+            if (at.unit == 0 && threadIdx.x == 0) kv_record(a, line, at, blockIdx.x, u, n_item, whole, u == u0);
             const long long piece = (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * 256 + t * 128 + r;
             const float f = l == 0.f ? 0.f : vpower * kv_code_scale<FMT>() / l;
             const float lse2 = l == 0.f ? -INFINITY : m - kKvPShift + log2f(l);
@@ -539,6 +543,8 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // the suffix may run beside the prefix; its completion, which the merge waits for, has to mean both
+  if (a.phase == kKvSuffix) pdl_wait();
 }
 
 }  // namespace fa
