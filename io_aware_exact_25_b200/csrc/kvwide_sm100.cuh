@@ -3,28 +3,40 @@
 //
 // An item tile is 256 rows (query tokens x heads of one key head's group) as
 // two 128-row tiles, the shape of the dense forward (fwd_sm100.cuh): tcgen05
-// MMAs S_t = Q_t K^T and O_t += P_t V accumulate in tensor memory, one softmax
-// thread per row, the two tiles taking turns on the tensor core.  What differs
-// is where K and V come from.  Warp roles:
-//   warps 0-3   softmax of tile 0 (they also load their rows of Q)
+// MMAs S_t = Q_t K^T and O_t += P_t V accumulate in tensor memory and the two
+// tiles take turns on the tensor core.  What differs is where K and V come
+// from.  Warp roles:
+//   warps 0-3   softmax of tile 0 (a thread per row; they also load Q)
 //   warps 4-7   softmax of tile 1
-//   warps 8-11  converter: codes from the cache's pages to f16 operand tiles
-//   warp  12    MMA issue (one thread); warps 13-15 complete its warpgroup
-// The converter threads load 16 codes at a time straight from the pages (one
-// tile ahead in registers, so the loads overlap the conversion), unpack them
-// exactly as the narrow kernel does and write the f16 tile in the 128-byte
-// swizzled layout the MMA reads: 256 rows share one conversion, under half an
-// instruction per code and row tile.  Inside each group of four the columns
-// stand in the order 0, 2, 1, 3, in which the codes unpack; Q is stored the
-// same way and O's columns are put back on the way out.
+//   warps 8-11  converter: codes to f16 operand tiles
+//   warp  12    MMA issue (one thread)
+//   warp  13    producer: codes and scales from the cache's pages to shared
+//               memory by bulk copies, a page (or 128 rows) at a time;
+//               warps 14-15 complete the warpgroup
+// The converter threads take 16 codes at a time, unpack them exactly as the
+// narrow kernel does and write the f16 tile in the 128-byte swizzled layout the
+// MMA reads: 256 rows share one conversion.  (They first loaded the codes
+// themselves, a tile ahead in registers; every load of a page number, a scale
+// or a tile then stood in the way of the next conversion, about 5000 clocks a
+// tile.)  Inside each
+// group of four the columns stand in the order 0, 2, 1, 3, in which the codes
+// unpack; Q is stored the same way and O's columns are put back at the end.
 //
-// Scales as in the narrow kernel: K's multiply the fp32 scores and V's, as
-// ratios to a running power of two, the probabilities.  The converter keeps
-// that power and publishes both scale vectors per tile of 128 keys.
+// Scales: K's multiply the fp32 scores, in the fma that also subtracts the
+// running maximum; the softmax scale is folded into them.  V's multiply the
+// codes during the conversion, as f16 ratios to a running power of two above
+// every V scale seen (two f16 roundings, 2^-11 each; with the factor
+// kv_v_shift the products stay in f16's normal range down to 2^-22 of the
+// largest scale).  A V scale that is NaN would spoil rows that do not see its
+// key, 0 x NaN: its row enters as zeros, and the rows that see it are made NaN
+// at the end, from a bit set of such keys per tile.  q goes into f16 as it is
+// if the row's largest entry is in [2^-2, 2^15), and shifted by a power of two
+// that its scores take back otherwise.
 //
-// The exponentials (one per score on the MUFU unit, 16 a clock) and the MMAs
-// (two of 128 x 128 x d per tile) take the same time at d = 128, 1024 clocks
-// a 128-row tile, so neither is far from its limit when the other is.
+// The scores of a row stay in its thread's registers: x = s ks - (m - 7) at
+// once, against the maximum so far, and only where some x exceeds 15 is m
+// raised and x shifted, so the usual tile costs one fma, half a max3, one
+// exponential, half an add and half a conversion per score.
 #pragma once
 
 #include "kvnarrow_sm100.cuh"
@@ -34,19 +46,25 @@ namespace fa {
 template <int D>
 struct KvWideLayout {
   static constexpr int kM = 256;
-  static constexpr int kThreads = 512;
-  // launched at 128 registers a thread: 2 x 128 x 184 + 128 x 104 + 128 x 40 = 512 x 128
-  static constexpr uint32_t kRegsSoftmax = 184, kRegsConvert = 104, kRegsCtl = 40;
-  static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsCtl <= 4 * 128, "register split");
+  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);
+  static constexpr int kConvert = 32 * kConvertWarps;
+  // launched at 128 registers a thread: 256 x 192 + 128 x 72 + 128 x 56 = 512 x 128
+  static constexpr uint32_t kRegsSoftmax = 192, kRegsConvert = 72, kRegsCtl = 56;
+  static_assert(256 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsCtl <= 128 * kThreads, "register split");
   static constexpr uint32_t kHalf = 128u * 128u;    // 128 rows x 64 f16 columns
   static constexpr uint32_t kTile = 128u * D * 2u;  // 128 x D f16
-  static constexpr int kStages = D == 128 ? 5 : 8;  // K/V operand ring
+  static constexpr int kStages = D == 128 ? 3 : 5;  // K/V operand ring
+  static constexpr int kRaw = D == 128 ? 3 : 5;     // ring of codes: K(j), V(j), K(j + 1), ...
+  static constexpr uint32_t kRawCodes = 128u * D;
+  static constexpr uint32_t kRawBytes = kRawCodes + 1024u;  // then 128 K scales and 128 V scales (K's slots only)
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = 2 * kTile;
-  static constexpr uint32_t kOffScale = kOffKV + kStages * kTile;  // 2 stages of 128 K scales, 128 V ratios
-  static constexpr uint32_t kOffMisc = kOffScale + 2 * 1024;       // [2] {V power, V NaN flag}, [2][4] warp maxima
-  static constexpr uint32_t kOffBar = kOffMisc + 2 * 8 + 8 * 4;
-  static constexpr int kNumBars = 2 + 2 * kStages + 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1;
+  static constexpr uint32_t kOffRaw = kOffKV + kStages * kTile;
+  static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawBytes;  // [2] 128 K scales times the softmax scale
+  static constexpr uint32_t kOffMisc = kOffScale + 2 * 512;        // [2] {V power, -, -, -, NaN keys [4]}, [2][4] maxima
+  static constexpr uint32_t kOffBar = kOffMisc + 2 * 32 + 2 * 16;
+  static constexpr int kNumBars = 2 + 2 * kStages + 2 * kRaw + 2 + 4 + 2 + 2 + 2 + 1 + 1;
   static constexpr uint32_t kOffScan = kOffBar + kNumBars * 8 + 16;
   static constexpr uint32_t kSmem = kOffScan + (uint32_t)sizeof(KvScan);
   static constexpr uint32_t kColO = 256;  // tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (D each)
@@ -54,10 +72,63 @@ struct KvWideLayout {
   static_assert(kOffScan % 8 == 0, "scan scratch alignment");
 };
 
+// V operands carry this power of two above code * ratio: 128 * 2^8 and 448 / 256 * 2^15 stay below f16's largest number.
+template <int FMT>
+__host__ __device__ constexpr float kv_v_shift() { return FMT == kKvInt8 ? 256.f : 32768.f; }
+
 // Instruction descriptor of kind::f16 with f16 inputs and fp32 accumulation (format codes 0; the other fields as
 // idesc_bf16).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Load 16 columns and wait for them.
+__device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  tmem_ld_wait();
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// The MMA warp's instructions, reached by all its lanes together and issued by the one that elect.sync names.  Where
+// the compiler sees a warp-uniform path and operands they go straight from uniform registers; issued from under
+// `lane == 0` the same MMAs took 116-216 clocks each whatever their size, against 64 of tensor-core time.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
@@ -65,23 +136,25 @@ __device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
+__global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(const KvArgs a) {
   using L = KvWideLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (through a shuffle: the roles' branches are then uniform to the compiler)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* bar_q = bars;                              // [2] Q_t written (128 arrivals)
   uint64_t* bar_kv_full = bars + 2;                    // [S] operand tile written (128)
   uint64_t* bar_kv_empty = bar_kv_full + L::kStages;   // [S] operand tile consumed
-  uint64_t* bar_s = bar_kv_empty + L::kStages;         // [2] S_t ready
-  uint64_t* bar_p = bar_s + 2;                         // [2] P_t written (128)
-  uint64_t* bar_pv = bar_p + 2;                        // [2] O_t += P_t V done
-  uint64_t* bar_p_half = bar_pv + 2;                   // [2] first half of P_t written (128)
-  uint64_t* bar_sc_full = bar_p_half + 2;              // [2] scales of a key tile written (128)
+  uint64_t* bar_raw_full = bar_kv_empty + L::kStages;  // [R] codes landed
+  uint64_t* bar_raw_empty = bar_raw_full + L::kRaw;    // [R] codes converted (4 warps)
+  uint64_t* bar_s = bar_raw_empty + L::kRaw;           // [2] S_t ready
+  uint64_t* bar_p = bar_s + 2;                         // [2][2] half h of P_t written (128)
+  uint64_t* bar_pv = bar_p + 4;                        // [2] O_t += P_t V done
+  uint64_t* bar_sc_full = bar_pv + 2;                  // [2] scales of a key tile written (128)
   uint64_t* bar_sc_empty = bar_sc_full + 2;            // [2] scales consumed (8 warps)
-  uint64_t* bar_drain = bar_sc_empty + 2;              //     every MMA retired
-  uint64_t* bar_vmax = bar_drain + 1;                  //     the converter warps' V maxima written (4 warps)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_vmax + 1);
+  uint64_t* bar_vmax = bar_sc_empty + 2;               //     the converter warps' V maxima written (4)
+  uint64_t* bar_drain = bar_vmax + 1;                  //     every MMA retired
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sscale = sbase + L::kOffScale, smisc = sbase + L::kOffMisc;
@@ -90,18 +163,22 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_q[t], 128);
       mbar_init(&bar_s[t], 1);
-      mbar_init(&bar_p[t], 128);
+      mbar_init(&bar_p[2 * t], 128);
+      mbar_init(&bar_p[2 * t + 1], 128);
       mbar_init(&bar_pv[t], 1);
-      mbar_init(&bar_p_half[t], 128);
       mbar_init(&bar_sc_full[t], 128);
-      mbar_init(&bar_sc_empty[t], 8);
+      mbar_init(&bar_sc_empty[t], L::kSoftmaxWarps);
     }
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&bar_kv_full[i], 128);
+      mbar_init(&bar_kv_full[i], L::kConvert);
       mbar_init(&bar_kv_empty[i], 1);
     }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&bar_raw_full[i], 1);
+      mbar_init(&bar_raw_empty[i], L::kConvertWarps);
+    }
+    mbar_init(bar_vmax, L::kConvertWarps);
     mbar_init(bar_drain, 1);
-    mbar_init(bar_vmax, 4);
     const bool misaligned = (sbase & 1023u) != 0u;
     *abort_flag = misaligned ? 1 : 0;
     if (misaligned && a.err) atomicCAS(a.err, kDevOk, kDevMisaligned);
@@ -115,15 +192,17 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
   int b;
   long long rem;
   const KvLine line =
-      kv_place<512>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem);
+      kv_place<L::kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Abort ab{abort_flag, a.err};
   const bool run = b >= 0 && *abort_flag == 0;
   if (a.phase == kKvWhole && threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;  // until this CTA leaves an item unfinished
-  const long long u0 = b >= 0 ? line.cut(blockIdx.x) : 0, u1 = b >= 0 ? line.cut(blockIdx.x + 1) : 0;
+  const int total = b >= 0 ? (int)(line.cut(blockIdx.x + 1) - line.cut(blockIdx.x)) : 0;  // this CTA's units
+  KvLine* s_line = reinterpret_cast<KvLine*>(smem + L::kOffScan);  // kept for kv_record only (the scan is over)
+  if (threadIdx.x == 0) *s_line = line;
   const int begin = kv_begin(a);
   KvSeq s{0, 0, 0};
   KvPlace at{0, 0, 0, 0};
@@ -135,199 +214,253 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
   // has rows.
   auto act1_of = [&]() { return (uint32_t)at.rt * 256u + 128u < (uint32_t)s.lq * (uint32_t)a.g; };
 
-  if (warp >= 12) {
+  if (warp >= L::kSoftmaxWarps + L::kConvertWarps) {
     regs_dec<L::kRegsCtl>();
-    if (run && warp == 12 && lane == 0) {
+    if (run && warp == L::kSoftmaxWarps + L::kConvertWarps) {
       // ------------------------------------------------------ MMA issue
       // Order for key tile j: O0 += P0 V(j-1), S0(j), O1 += P1 V(j-1), S1(j), as in the dense forward: S_t(j)
       // overwrites the columns of P_t(j-1) behind the product that reads them, and a completed S_t(j) implies that
       // O_t holds every earlier product.
       constexpr uint32_t kIdS = idesc_f16(128, 128, false);
       constexpr uint32_t kIdO = idesc_f16(128, D, true);
-      uint32_t pos = 0;             // operand ring position: K(j) then V(j), over all items
-      uint32_t nq[2] = {0, 0};      // items of each row tile so far
-      uint32_t np[2] = {0, 0};      // P tiles of each row tile so far
+      uint32_t pos = 0;           // operand ring position: K(j) then V(j), over all items
+      uint32_t nq0 = 0, nq1 = 0;  // items of each row tile so far
+      uint32_t np0 = 0, np1 = 0;  // P tiles of each row tile so far
       bool ok = true, issued = false;
-      auto full = [&](uint32_t p) { return mbar_wait(&bar_kv_full[p % L::kStages], (p / L::kStages) & 1u, ab); };
-      auto tile_of = [&](uint32_t p) { return sbase + L::kOffKV + (p % L::kStages) * L::kTile; };
-      auto issue_s = [&](int t, uint32_t sK) {
-        const uint32_t sQ = sbase + L::kOffQ + t * L::kTile;
+      auto full = [&](uint32_t p) { return mbar_wait_warp(&bar_kv_full[p % L::kStages], (p / L::kStages) & 1u, ab); };
+      // Descriptors of slice 0; a slice further on is a constant added to the address field (addresses stay below
+      // 2^18, so nothing carries out of it).
+      const uint64_t dq0 = desc_kmajor(sbase + L::kOffQ, 0, L::kHalf);
+      const uint64_t dk0 = desc_kmajor(sbase + L::kOffKV, 0, L::kHalf);
+      const uint64_t dv0 = desc_mnmajor(sbase + L::kOffKV, 0, L::kHalf);
+      auto stage_step = [](uint32_t p) { return (uint64_t)((p % L::kStages) * (L::kTile >> 4)); };
+      auto issue_s = [&](int t, uint32_t p) {
+        uint64_t dq = dq0 + (uint64_t)(t * (L::kTile >> 4)), dk = dk0 + stage_step(p);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + 128u * t, desc_kmajor(sQ, kk, L::kHalf), desc_kmajor(sK, kk, L::kHalf), kIdS, kk > 0 ? 1u : 0u);
-        mma_commit(&bar_s[t]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          mma_ss_elect(tmem + 128u * t, dq, dk, kIdS, kk > 0 ? 1u : 0u);
+          const uint64_t step = kk == 3 ? (uint64_t)((L::kHalf - 96u) >> 4) : 2ull;  // the next 16 columns
+          dq += step;
+          dk += step;
+        }
+        mma_commit_elect(&bar_s[t]);
         issued = true;
       };
-      auto issue_pv = [&](int t, bool first, uint32_t sV) -> bool {
-        const uint32_t ph = np[t]++ & 1u;
-        if (!mbar_wait(&bar_p_half[t], ph, ab)) return false;
-        tc_fence_after();
+      auto issue_pv = [&](int t, bool first, uint32_t p) -> bool {
+        uint64_t dv = dv0 + stage_step(p);
+        const uint32_t ph = (t ? np1++ : np0++) & 1u;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts(tmem + L::kColO + D * t, tmem + 128u * t + 8u * kk, desc_mnmajor(sV, kk, L::kHalf), kIdO,
-                 (!first || kk > 0) ? 1u : 0u);
-        if (!mbar_wait(&bar_p[t], ph, ab)) return false;
-        tc_fence_after();
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait_warp(&bar_p[2 * t + h], ph, ab)) return false;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 4; kk < 8; ++kk)
-          mma_ts(tmem + L::kColO + D * t, tmem + 128u * t + 8u * kk, desc_mnmajor(sV, kk, L::kHalf), kIdO, 1u);
-        mma_commit(&bar_pv[t]);
+          for (int kk = 0; kk < 4; ++kk) {
+            mma_ts_elect(tmem + L::kColO + D * t, tmem + 128u * t + 32u * h + 8u * kk, dv, kIdO,
+                   (!first || h > 0 || kk > 0) ? 1u : 0u);
+            dv += 2048u >> 4;  // 16 keys further down
+          }
+        }
+        mma_commit_elect(&bar_pv[t]);
         return true;
       };
-      for (long long u = u0; u < u1 && ok;) {
-        const int n = (int)min((long long)(kv_item_units(a, s, at.rt) - at.unit), u1 - u);
+      for (int left = total; left > 0 && ok;) {
+        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
         const int nt = act1_of() ? 2 : 1;
-        for (int t = 0; t < nt && ok; ++t) ok = mbar_wait(&bar_q[t], nq[t]++ & 1u, ab);
+#pragma unroll 1
+        for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_warp(&bar_q[t], (t ? nq1++ : nq0++) & 1u, ab);
+#pragma unroll 1
         for (int j = 0; j <= n && ok; ++j) {
           // tiles in hand: K(j) at pos + 2 j, V(j - 1) at pos + 2 j - 1
           const uint32_t pk = pos + 2u * j, pv = pk - 1u;
           if (j > 0 && !(ok = full(pv))) break;
           if (j < n && !(ok = full(pk))) break;
           tc_fence_after();
+#pragma unroll 1
           for (int t = 0; t < nt && ok; ++t) {
-            if (j > 0) ok = issue_pv(t, j == 1, tile_of(pv));
-            if (ok && j < n) issue_s(t, tile_of(pk));
+            if (j > 0) ok = issue_pv(t, j == 1, pv);
+            if (ok && j < n) issue_s(t, pk);
           }
           if (!ok) break;
-          if (j > 0) mma_commit(&bar_kv_empty[pv % L::kStages]);
-          if (j < n) mma_commit(&bar_kv_empty[pk % L::kStages]);
+          if (j > 0) mma_commit_elect(&bar_kv_empty[pv % L::kStages]);
+          if (j < n) mma_commit_elect(&bar_kv_empty[pk % L::kStages]);
         }
         pos += 2u * n;
-        u += n;
-        if (u < u1 && !kv_next(a, s, at)) break;
+        left -= n;
+        if (left > 0 && !kv_next(a, s, at)) break;
       }
       if (issued) {
-        mma_commit(bar_drain);
+        mma_commit_elect(bar_drain);
         mbar_wait_drain(bar_drain, 0);
       }
     }
-  } else if (warp >= 8) {
-    regs_dec<L::kRegsConvert>();
-    if (run) {
-      // ------------------------------------------------------ converter
-      constexpr int CH = D / 16;        // 16-code chunks of a row
-      constexpr int RP = 128 / CH;      // rows the 128 threads cover in one pass
-      constexpr int NP = 128 / RP;      // passes of a tile
-      const int tid = threadIdx.x - 256;
-      const int cw = warp - 8;
-      const int ch = tid % CH, r_in = tid / CH;
-      // the chunk's place in row r of the operand tile: 16 f16 columns are two 16-byte chunks of the 64-column half
-      // ch / 4; lanes of the upper half write the second one first, so that eight lanes cover all banks
-      const uint32_t half_off = (uint32_t)(ch >> 2) * L::kHalf;
-      const int c0 = 2 * (ch & 3);
-      const int swap = D == 128 ? (ch >> 2) & 1 : r_in & 1;
-      uint32_t pos = 0, nsc = 0;
+    if (run && warp == L::kSoftmaxWarps + L::kConvertWarps + 1) {
+      // ------------------------------------------------------- producer
+      // Lane l brings rows [l g, (l + 1) g) of a tile, g = min(page size, 128): they are contiguous in their page.
+      // Rows past the item's keys are not asked for unless they share a page with a key; what the slot held before
+      // stands in for them (any code is finite, and the converter gives such keys scale 0).
+      const int g = min(1 << a.page_shift, 128);
+      uint32_t pos = 0;
       bool ok = true;
-      for (long long u = u0; u < u1 && ok;) {
-        const int n = (int)min((long long)(kv_item_units(a, s, at.rt) - at.unit), u1 - u);
+      for (int left = total; left > 0 && ok;) {
+        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
         const int item_end = kv_item_end(a, s, at.rt);
         const int first = begin + at.unit * kKvUnit;
         const int* trow = a.table + (a.phase == kKvPrefix ? 0ll : at.b * a.table_stride);
-        float vpower = 1.1754943508222875e-38f;
-        // lane l < 8 of each warp: cache row of the first of keys 16 l .. 16 l + 15 of a tile; -1 past the keys
-        auto fetch_rows = [&](int j) -> int {
-          const int key = first + j * kKvUnit + 16 * (lane & 7);
-          if (j >= n || key >= item_end) return -1;
-          int page = __ldg(trow + (key >> a.page_shift));
-          if (page < 0 || page >= a.num_pages) {
+        auto fetch = [&](int j) -> int {  // this lane's cache row in tile j, or -1
+          const int key = first + j * kKvUnit + g * lane;
+          return j < n && g * lane < 128 && key < item_end ? __ldg(trow + (key >> a.page_shift)) : -1;
+        };
+        int page_next = fetch(0);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int key = first + j * kKvUnit + g * lane;
+          const bool mine = g * lane < 128 && key < item_end;
+          int page = page_next;
+          page_next = fetch(j + 1);
+          if (mine && (page < 0 || page >= a.num_pages)) {
             if (a.err) atomicCAS(a.err, kDevOk, kDevBadPage);
             page = 0;
           }
           const long long row = (((long long)page * a.Hkv + at.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-          return FA_IN(kSiteKvRow, row, 16, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err) ? (int)row : -1;
-        };
-        auto load_tile = [&](const uint8_t* codes, int rows, uint4 (&raw)[NP]) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const int r = i * RP + r_in;  // row of the tile; its group of 16 is the same for the whole warp
-            const int base = __shfl_sync(0xffffffffu, rows, r >> 4);
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (base >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(codes + ((long long)base + (r & 15)) * D) + ch);
+          const bool in = mine && FA_IN(kSiteKvRow, row, g, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err);
+          const uint32_t rows = (uint32_t)g * (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
+#pragma unroll 1
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t sl = pos % L::kRaw;
+            if (!(ok = mbar_wait_warp(&bar_raw_empty[sl], ((pos / L::kRaw) & 1u) ^ 1u, ab))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar_raw_full[sl], rows * (uint32_t)(which ? D : D + 8));
+            __syncwarp();
+            uint8_t* dst = smem + L::kOffRaw + sl * L::kRawBytes;
+            if (in) {
+              bulk_load(dst + g * lane * D, (which ? a.v : a.k) + row * D, (uint32_t)(g * D), &bar_raw_full[sl]);
+              if (which == 0) {
+                bulk_load(dst + L::kRawCodes + 4 * g * lane, a.ks + row, 4u * g, &bar_raw_full[sl]);
+                bulk_load(dst + L::kRawCodes + 512 + 4 * g * lane, a.vs + row, 4u * g, &bar_raw_full[sl]);
+              }
+            }
+            ++pos;
           }
-        };
-        auto store_tile = [&](const uint4 (&raw)[NP]) -> bool {
-          const uint32_t st = pos % L::kStages;
+        }
+        left -= n;
+        if (left > 0 && !kv_next(a, s, at)) break;
+      }
+      // every copy asked for lands before the CTA may exit
+      for (uint32_t p = pos > L::kRaw ? pos - L::kRaw : 0u; p < pos; ++p)
+        mbar_wait_drain(&bar_raw_full[p % L::kRaw], (p / L::kRaw) & 1u);
+    }
+  } else if (warp >= L::kSoftmaxWarps) {
+    regs_dec<L::kRegsConvert>();
+    if (run) {
+      // ------------------------------------------------------ converter
+      constexpr int CH = D / 16;           // 16-code chunks of a row
+      constexpr int RP = L::kConvert / CH; // rows the threads cover in one pass
+      constexpr int NP = 128 / RP;         // passes of a tile
+      const int tid = threadIdx.x - 32 * L::kSoftmaxWarps;
+      const int cw = warp - L::kSoftmaxWarps;
+      const int ch = tid % CH, r_in = tid / CH;
+      // the chunk's place in row r of the operand tile: 16 f16 columns are two 16-byte chunks of the 64-column half
+      // ch / 4.  At d = 128 eight lanes store one row, and those of the upper half write the second one first, so that
+      // the eight cover all banks; at d = 64 they store two rows, whose swizzles differ already.
+      const uint32_t half_off = (uint32_t)(ch >> 2) * L::kHalf;
+      const int c0 = 2 * (ch & 3);
+      const int swap = D == 128 ? (ch >> 2) & 1 : 0;
+      uint32_t pos = 0, nsc = 0;
+      bool ok = true;
+      for (int left = total; left > 0 && ok;) {
+        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
+        const int item_end = kv_item_end(a, s, at.rt);
+        const int first = begin + at.unit * kKvUnit;
+        float vpower = 1.1754943508222875e-38f;
+        // the next tile of codes, converted; rows' factors if it is V's
+        auto convert = [&](const uint32_t* ratio) -> bool {
+          const uint32_t st = pos % L::kStages, sl = pos % L::kRaw;
+          const uint32_t src = sbase + L::kOffRaw + sl * L::kRawBytes + ch * 16;
+          if (ratio && !mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab)) return false;
+          uint4 raw[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) raw[i] = ld_shared_u4(src + (i * RP + r_in) * D);
           if (!mbar_wait_warp(&bar_kv_empty[st], ((pos / L::kStages) & 1u) ^ 1u, ab)) return false;
           const uint32_t tile = sbase + L::kOffKV + st * L::kTile + half_off;
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             const int r = i * RP + r_in;
-            uint32_t e[4], o[4];
-            kv_unpack<FMT>(raw[i].x, e[0], o[0]);
-            kv_unpack<FMT>(raw[i].y, e[1], o[1]);
-            kv_unpack<FMT>(raw[i].z, e[2], o[2]);
-            kv_unpack<FMT>(raw[i].w, e[3], o[3]);
+            uint32_t w[8];
+            kv_unpack<FMT>(raw[i].x, w[0], w[1]);
+            kv_unpack<FMT>(raw[i].y, w[2], w[3]);
+            kv_unpack<FMT>(raw[i].z, w[4], w[5]);
+            kv_unpack<FMT>(raw[i].w, w[6], w[7]);
+            if (ratio) {
+              const __half2 f = *reinterpret_cast<const __half2*>(&ratio[i]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), f);
+                w[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+            }
             const uint32_t row = tile + r * 128;
-            const uint32_t a0 = row + (((c0 + swap) ^ (r & 7)) << 4), a1 = row + (((c0 + 1 - swap) ^ (r & 7)) << 4);
+            const uint32_t a0 = row + ((c0 ^ (r & 7)) << 4), a1 = row + (((c0 + 1) ^ (r & 7)) << 4);
             if (swap) {
-              st_shared_v4(a0, e[2], o[2], e[3], o[3]);
-              st_shared_v4(a1, e[0], o[0], e[1], o[1]);
+              st_shared_v4(a1, w[4], w[5], w[6], w[7]);
+              st_shared_v4(a0, w[0], w[1], w[2], w[3]);
             } else {
-              st_shared_v4(a0, e[0], o[0], e[1], o[1]);
-              st_shared_v4(a1, e[2], o[2], e[3], o[3]);
+              st_shared_v4(a0, w[0], w[1], w[2], w[3]);
+              st_shared_v4(a1, w[4], w[5], w[6], w[7]);
             }
           }
           fence_proxy_async_smem();
           mbar_arrive(&bar_kv_full[st]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_raw_empty[sl]);
           ++pos;
           return true;
         };
-        auto load_scale = [&](const float* sc, int rows) -> float {
-          const int base = __shfl_sync(0xffffffffu, rows, tid >> 4);
-          return base >= 0 ? __ldg(sc + base + (tid & 15)) : 0.f;
-        };
-        uint4 rk[NP], rv[NP];
-        int rows = fetch_rows(0);
-        load_tile(a.k, rows, rk);
-        load_tile(a.v, rows, rv);
-        float ks = load_scale(a.ks, rows), vs = load_scale(a.vs, rows);
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int next = fetch_rows(j + 1);
-          // scales of this tile
-          const bool in = first + j * kKvUnit + tid < item_end;
-          uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
-          const bool vnan = in && vb > 0x7f800000u;
-          if (!in || vb >= 0x7f800000u) vb = 0u;
-          const uint32_t wmax = __reduce_max_sync(0xffffffffu, vb);
-          const bool wnan = __any_sync(0xffffffffu, vnan);
-          // the four warps' maxima meet (a bounded wait, so that an aborting CTA cannot strand a warp at a barrier)
-          const uint32_t red = smisc + 16 + (nsc & 1u) * 16;
+          const uint32_t sl = pos % L::kRaw;
+          if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
+          const uint32_t raw_sc = sbase + L::kOffRaw + sl * L::kRawBytes + L::kRawCodes;
+          const int key0 = first + j * kKvUnit;
+          const bool in = key0 + tid < item_end;
+          const float ks = in ? ld_shared_f(raw_sc + 4 * tid) : 0.f;
+          const float vk = in ? ld_shared_f(raw_sc + 512 + 4 * tid) : 0.f;
+          float vs[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vs[i] = ld_shared_f(raw_sc + 512 + 4 * (i * RP + r_in));
+          // the largest V scale of the tile: each warp leaves its own, all read (a bounded wait, so that an aborting CTA
+          // cannot strand a warp at a barrier)
+          const uint32_t red = smisc + 64 + (nsc & 1u) * 16;
+          const uint32_t vb = __float_as_uint(vk) & 0x7fffffffu;
+          const uint32_t vnan = __ballot_sync(0xffffffffu, vb > 0x7f800000u);
+          const uint32_t wmax = __reduce_max_sync(0xffffffffu, vb >= 0x7f800000u ? 0u : vb);
           if (lane == 0) {
-            st_shared_f(red + 4 * cw, __uint_as_float(wmax | (wnan ? 0x80000000u : 0u)));
+            st_shared_f(red + 4 * cw, __uint_as_float(wmax));
             mbar_arrive(bar_vmax);
           }
           if (!(ok = mbar_wait_warp(bar_vmax, nsc & 1u, ab))) break;
-          const float4 m4 = ld_shared_f4(red);
-          const uint32_t mb[4] = {__float_as_uint(m4.x), __float_as_uint(m4.y), __float_as_uint(m4.z), __float_as_uint(m4.w)};
-          uint32_t vmax = 0u, anynan = 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vmax = max(vmax, mb[i] & 0x7fffffffu);
-            anynan |= mb[i] & 0x80000000u;
-          }
+          const float4 m4 = ld_shared_f4(red);  // all positive: as integers they sort alike
+          const uint32_t vmax = max(max(__float_as_uint(m4.x), __float_as_uint(m4.y)),
+                                    max(__float_as_uint(m4.z), __float_as_uint(m4.w)));
           if (vmax > __float_as_uint(vpower))
             vpower = __uint_as_float(min((vmax & 0x7f800000u) + 0x00800000u, 0x7e800000u));
           const float vinv = __uint_as_float((254u << 23) - __float_as_uint(vpower));
+          uint32_t ratio[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float f = key0 + i * RP + r_in < item_end ? vs[i] * vinv * kv_v_shift<FMT>() : 0.f;
+            ratio[i] = f == f ? pack_f16x2(f, f) : 0u;
+          }
           const uint32_t st = nsc & 1u;
           if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
-          st_shared_f(sscale + st * 1024 + 4 * tid, in ? ks : 0.f);
-          st_shared_f(sscale + st * 1024 + 512 + 4 * tid, in ? vs * vinv : 0.f);
-          if (tid == 0) {
-            st_shared_f(smisc + st * 8, vpower);
-            st_shared_f(smisc + st * 8 + 4, anynan ? 1.f : 0.f);
-          }
+          st_shared_f(sscale + st * 512 + 4 * tid, ks * (a.scale_log2 * kv_code_scale<FMT>()));
+          if (lane == 0) st_shared_f(smisc + st * 32 + 16 + 4 * cw, __uint_as_float(vnan));
+          if (tid == 0) st_shared_f(smisc + st * 32, vpower);
           mbar_arrive(&bar_sc_full[st]);
           ++nsc;
-          // the next tile's loads go out behind each conversion
-          if (!(ok = store_tile(rk))) break;
-          load_tile(a.k, next, rk);
-          ks = load_scale(a.ks, next);
-          vs = load_scale(a.vs, next);
-          if (!(ok = store_tile(rv))) break;
-          load_tile(a.v, next, rv);
+          if (!(ok = convert(nullptr))) break;
+          if (!(ok = convert(ratio))) break;
         }
-        u += n;
-        if (u < u1 && !kv_next(a, s, at)) break;
+        left -= n;
+        if (left > 0 && !kv_next(a, s, at)) break;
       }
     }
   } else {
@@ -341,22 +474,21 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
       const uint32_t tO = tmem + lane_off + L::kColO + D * t;
       uint32_t ns = 0, nsc = 0;  // score tiles and scale stages so far
       bool ok = true;
-      for (long long u = u0; u < u1 && ok;) {
+      for (int left = total; left > 0 && ok;) {
         const int n_item = kv_item_units(a, s, at.rt);
-        const int n = (int)min((long long)(n_item - at.unit), u1 - u);
+        const int n = min(n_item - at.unit, left);
         const int first = begin + at.unit * kKvUnit;
         if (t == 1 && !act1_of()) {
           // no rows here: only release the scales
           for (int j = 0; j < n && ok; ++j, ++nsc) {
             ok = mbar_wait_warp(&bar_sc_full[nsc & 1u], (nsc >> 1) & 1u, ab);
-            __syncwarp();
             if (ok && lane == 0) mbar_arrive(&bar_sc_empty[nsc & 1u]);
           }
         } else {
           const KvRow x = kv_row_of(a, s, at.h, at.rt, t * 128 + r);
-          float qs = 0.f;
+          float up = 1.f;
           {
-            // this thread's row of Q as f16 times 2^-e, columns in the order the codes unpack
+            // this thread's row of Q as f16, columns in the order the codes unpack
             const long long qo = x.token * a.q_sn + x.head * a.q_sh;
             const bool in =
                 x.token >= 0 && FA_IN(kSiteKvQ, qo, D, extent4(1, a.Hq, a.total, D, 0, a.q_sh, a.q_sn), a.err);
@@ -364,16 +496,14 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
             uint4 w[D / 8];
             uint32_t m2 = 0u;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              w[c] = in ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int c = 0; c < D / 8; ++c) w[c] = in ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
               m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu),
                                          __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu)));
-            float down, up;
-            kv_q_shift(__uint_as_float(max(m2 & 0xffffu, m2 >> 16) << 16), down, up);
-            qs = up * a.scale_log2 * kv_code_scale<FMT>();
+            const float amax = __uint_as_float(max(m2 & 0xffffu, m2 >> 16) << 16);
+            float down = 1.f;
+            if (!(amax == 0.f || (amax >= 0.25f && amax < 32768.f))) kv_q_shift(amax, down, up);
             const uint32_t row = sbase + L::kOffQ + t * L::kTile + r * 128;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
@@ -385,41 +515,71 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
             fence_proxy_async_smem();
             mbar_arrive(&bar_q[t]);
           }
-          float m = -INFINITY, l = 0.f, vpower = 0.f;
+          const bool shifted = __any_sync(0xffffffffu, up != 1.f);
+          float m = 0.f, l = 0.f, vpower = 0.f;  // m means nothing while l = 0
+          bool spoiled = false;                  // the row sees a key whose V scale is NaN
+#pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const uint32_t st = nsc & 1u;
             if (!(ok = mbar_wait_warp(&bar_sc_full[st], (nsc >> 1) & 1u, ab))) break;
             if (!(ok = mbar_wait_warp(&bar_s[t], ns & 1u, ab))) break;
             tc_fence_after();
-            const uint32_t sK = sscale + st * 1024, sV = sK + 512;
-            const float vp = ld_shared_f(smisc + st * 8);
-            const bool vnan = ld_shared_f(smisc + st * 8 + 4) != 0.f;
+            const uint32_t sK = sscale + st * 512;
+            const float vp = ld_shared_f(smisc + st * 32);
+            const int lim = x.end - (first + j * kKvUnit);  // of the tile's keys, those below it are visible
+            const float4 nan4 = ld_shared_f4(smisc + st * 32 + 16);
             uint32_t w[4][32];
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + 32u * c4, w[c4]);
             tmem_ld_wait();
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) reg_fence(w[c4]);
-            // scores times K scales
-            auto scale_k = [&]() {
+            if (shifted) {
 #pragma unroll
-              for (int c = 0; c < 128; c += 4) {
-                const float4 k4 = ld_shared_f4(sK + 4 * c);
-                uint32_t* p = &w[c >> 5][c & 31];
+              for (int c = 0; c < 128; ++c) w[c >> 5][c & 31] = __float_as_uint(__uint_as_float(w[c >> 5][c & 31]) * up);
+            }
+            const uint64_t sub2 = f2_pack(kKvPShift - m, kKvPShift - m);
+            // 16 K scales ahead of those in use: one at a time, each load's latency stood in the way
+            float4 k4[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k4[0][i] = ld_shared_f4(sK + 16 * i);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              if (g < 7) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k4[(g + 1) & 1][i] = ld_shared_f4(sK + 64 * (g + 1) + 16 * i);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 k = k4[g & 1][i];
+                uint32_t* p = &w[g >> 1][16 * (g & 1) + 4 * i];
                 float y[4];
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1])), f2_pack(k4.x, k4.y)), y[0], y[1]);
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3])), f2_pack(k4.z, k4.w)), y[2], y[3]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1])), f2_pack(k.x, k.y), sub2), y[0],
+                          y[1]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3])), f2_pack(k.z, k.w), sub2), y[2],
+                          y[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) p[e] = __float_as_uint(y[e]);
               }
-            };
-            scale_k();
-            const int lim = x.end - (first + j * kKvUnit);  // keys below it are visible
-            const bool masked = __any_sync(0xffffffffu, lim < 128);
-            if (masked) {
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
+            if (__any_sync(0xffffffffu, lim < 128)) {
 #pragma unroll
               for (int c = 0; c < 128; ++c)
                 if (c >= lim) w[c >> 5][c & 31] = 0xff800000u;
+            }
+            {
+              // keys with a NaN V scale: does the row see one?
+              const uint32_t nb[4] = {__float_as_uint(nan4.x), __float_as_uint(nan4.y), __float_as_uint(nan4.z),
+                                      __float_as_uint(nan4.w)};
+              if ((nb[0] | nb[1] | nb[2] | nb[3]) != 0u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int k = lim - 32 * i;
+                  spoiled |= (nb[i] & (k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0u;
+                }
+              }
             }
             float mx4[4];
 #pragma unroll
@@ -430,77 +590,52 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
               for (int g = 0; g < 4; ++g) mx4[g] = max3(mx4[g], __uint_as_float(w[g][c]), __uint_as_float(w[g][c + 1]));
 #pragma unroll
             for (int g = 0; g < 4; ++g) mx4[g] = fmaxf(mx4[g], __uint_as_float(w[g][31]));
-            const float m_new = fmaxf(m, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs);
-            if (__any_sync(0xffffffffu, m_new > m + 8.f) || vp != vpower) {
-              const float alpha = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            // the first visible scores of a row set its maximum, later ones raise it by what they exceed it
+            const bool fresh = l == 0.f && mx != -INFINITY;
+            const bool raise = fresh || mx > 8.f + kKvPShift;
+            if (__any_sync(0xffffffffu, raise) || vp != vpower) {
+              const float delta = raise ? mx - kKvPShift : 0.f;
+              const float alpha = fresh ? 1.f : ex2(-delta);
+              m += delta;
               l *= alpha;
-              m = m_new;
+#pragma unroll
+              for (int c = 0; c < 128; ++c) w[c >> 5][c & 31] = __float_as_uint(__uint_as_float(w[c >> 5][c & 31]) - delta);
               if (j > 0) {
-                // O_t holds the sum over the earlier tiles (their products completed before S_t(j)); the score
-                // registers are released for the rescale and read again after it
+                // O_t holds the sum over the earlier tiles (their products completed before S_t(j)), and none is
+                // added before P is published
                 const float f = alpha * vpower * __uint_as_float((254u << 23) - __float_as_uint(vp));
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_sync(tO + c, o);
 #pragma unroll
-                for (int c4 = 0; c4 < D / 32; ++c4) {
-                  uint32_t o[32];
-                  tmem_ld32_sync(tO + 32u * c4, o);
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                  tmem_st32(tO + 32u * c4, o);
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tmem_st16(tO + c, o);
                 }
                 tmem_st_wait();
-#pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + 32u * c4, w[c4]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) reg_fence(w[c4]);
-                scale_k();
-                if (masked) {
-#pragma unroll
-                  for (int c = 0; c < 128; ++c)
-                    if (c >= lim) w[c >> 5][c & 31] = 0xff800000u;
-                }
               }
               vpower = vp;
             }
-            const float sub = (m == -INFINITY ? 0.f : m) - kKvPShift;
-            const uint64_t mul2 = f2_pack(qs, qs), sub2 = f2_pack(-sub, -sub);
             uint64_t sum2[2] = {0ull, 0ull};
-            // P in f16 pairs, 64 keys at a time; the product starts on the first half
+            // P in f16 pairs, 64 keys at a time: the product starts on the first half
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint32_t pk[32];
 #pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                const float4 v4 = ld_shared_f4(sV + 4 * (64 * h + c));
-                const uint32_t* p = &w[(64 * h + c) >> 5][c & 31];
-                float x0, x1, p0, p1, p2, p3;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1])), mul2, sub2), x0, x1);
-                p0 = ex2(x0), p1 = ex2(x1);
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3])), mul2, sub2), x0, x1);
-                p2 = ex2(x0), p3 = ex2(x1);
-                const uint64_t q0 = f2_pack(p0, p1), q1 = f2_pack(p2, p3);
-                sum2[0] = f2_add(sum2[0], q0);
-                sum2[1] = f2_add(sum2[1], q1);
-                f2_unpack(f2_mul(q0, f2_pack(v4.x, v4.y)), p0, p1);
-                f2_unpack(f2_mul(q1, f2_pack(v4.z, v4.w)), p2, p3);
-                pk[c / 2] = pack_f16x2(p0, p1);
-                pk[c / 2 + 1] = pack_f16x2(p2, p3);
-              }
-              if (masked && vnan) {
-                // a NaN V scale times the zero probability of a hidden key
+              for (int g = 0; g < 2; ++g) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  if (64 * h + 2 * c >= lim) pk[c] = 0u;
-                  else if (64 * h + 2 * c + 1 >= lim) pk[c] &= 0xffffu;
+                for (int c = 0; c < 16; ++c) {
+                  const float p0 = ex2(__uint_as_float(w[2 * h + g][2 * c])), p1 = ex2(__uint_as_float(w[2 * h + g][2 * c + 1]));
+                  sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
+                  pk[c] = pack_f16x2(p0, p1);
                 }
+                tmem_st16(tS + 32u * h + 16u * g, pk);
               }
-              tmem_st32(tS + 32u * h, pk);
               tmem_st_wait();
               tc_fence_before();
-              mbar_arrive(h == 0 ? &bar_p_half[t] : &bar_p[t]);
+              mbar_arrive(&bar_p[2 * t + h]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
             {
               float s0, s1, s2, s3;
               f2_unpack(sum2[0], s0, s1);
@@ -514,25 +649,27 @@ __global__ void __launch_bounds__(512, 1) kv_wide_kernel(const KvArgs a) {
           if (ok) {
             tc_fence_after();
             const bool whole = at.unit == 0 && n == n_item;
-            if (at.unit == 0 && threadIdx.x == 0) kv_record(a, line, at, blockIdx.x, u, n_item, whole, u == u0);
-            const long long piece = (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * 256 + t * 128 + r;
-            const float f = l == 0.f ? 0.f : vpower * kv_code_scale<FMT>() / l;
+            if (at.unit == 0 && threadIdx.x == 0)
+              kv_record(a, *s_line, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left), n_item, whole, left == total);
+            const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + t * 128 + r;
+            float f = l == 0.f ? 0.f : vpower * (kv_code_scale<FMT>() / kv_v_shift<FMT>()) / l;
+            if (spoiled) f = __uint_as_float(0x7fc00000u);
             const float lse2 = l == 0.f ? -INFINITY : m - kKvPShift + log2f(l);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_sync(tO + c, o);
+              float v[16];
 #pragma unroll
-            for (int c4 = 0; c4 < D / 32; ++c4) {
-              uint32_t o[32];
-              tmem_ld32_sync(tO + 32u * c4, o);
-              float v[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k)  // columns 1 and 2 of each four change places
+              for (int k = 0; k < 16; ++k)  // columns 1 and 2 of each four change places
                 v[(k & ~3) | ((k & 1) << 1) | ((k >> 1) & 1)] = __uint_as_float(o[k]) * f;
-              if (x.token >= 0) kv_put_row<D, 32>(a, x, whole, piece, 2ll * gridDim.x * 256, 32 * c4, v, lse2);
+              if (x.token >= 0) kv_put_row<D, 16>(a, x, whole, piece, 2ll * gridDim.x * 256, c, v, lse2);
             }
             tc_fence_before();
           }
         }
-        u += n;
-        if (u < u1 && !kv_next(a, s, at)) break;
+        left -= n;
+        if (left > 0 && !kv_next(a, s, at)) break;
       }
     }
   }
