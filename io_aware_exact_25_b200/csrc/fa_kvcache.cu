@@ -138,26 +138,23 @@ int make_code_map(CUtensorMap* m, const void* base, const fa_kv_cache* c, int bo
 
 constexpr int kSms = 148;
 
-template <int D, int MT>
-struct NarrowOf;
-template <>
-struct NarrowOf<128, 1> { using L = fa::KvNarrowLayout<128, 1, 3, 2>; };
-template <>
-struct NarrowOf<128, 2> { using L = fa::KvNarrowLayout<128, 2, 3, 2>; };
-template <>
-struct NarrowOf<64, 1> { using L = fa::KvNarrowLayout<64, 1, 4, 3>; };
-template <>
-struct NarrowOf<64, 2> { using L = fa::KvNarrowLayout<64, 2, 4, 2>; };
+// Ring depth and CTAs per SM of the narrow kernel.  (Three CTAs of two slices a warp at d = 128, 168 registers a
+// thread: the same time, 143 us for 64 sequences of 512 to 8192 keys and 8 key heads; two of three slices: the same.)
+template <int D>
+using Narrow = fa::KvNarrowLayout<D, D == 128 ? 2 : 3, D == 128 ? 2 : 3>;
 
 // The kernel for items of `rows` rows: rows per item tile and stretches the work is cut into.
 struct Choice {
   int M, G;
+  int item_cost;  // starting and ending an item, in units of 128 keys
 };
 
 Choice choose(long long rows, int d) {
-  if (rows <= 16) return {16, kSms * (d == 128 ? NarrowOf<128, 1>::L::kCtasPerSm : NarrowOf<64, 1>::L::kCtasPerSm)};
-  if (rows <= 32) return {32, kSms * (d == 128 ? NarrowOf<128, 2>::L::kCtasPerSm : NarrowOf<64, 2>::L::kCtasPerSm)};
-  return {256, kSms};
+  // Up to 16 rows one mma.sync tile holds an item and the cache's bytes are what is waited for.  Above, the wide
+  // kernel: a 32-row narrow one spilled and was slower or no faster (24 heads over one key head, 8 sequences of 512
+  // to 8192 keys: 44 us against 32; 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 254 against 266).
+  if (rows <= 16) return {16, kSms * (d == 128 ? Narrow<128>::kCtasPerSm : Narrow<64>::kCtasPerSm), 2};
+  return {256, kSms, 3};
 }
 
 // Byte offsets in the workspace: the pieces of one launch and the entries that say where they are.
@@ -226,10 +223,10 @@ int launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t
   return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT>
 int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
-  using L = typename NarrowOf<D, MT>::L;
-  auto kern = fa::kv_narrow_kernel<D, FMT, MT, L>;
+  using L = Narrow<D>;
+  auto kern = fa::kv_narrow_kernel<D, FMT, L>;
   CUtensorMap mk, mv;
   const int box = c->page_size < 32 ? c->page_size : 32;
   int rc;
@@ -251,8 +248,7 @@ int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
 
 template <int D, int FMT>
 int launch_phase_as(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
-  if (ch.M == 16) return launch_narrow<D, FMT, 1>(c, a, ch, st);
-  if (ch.M == 32) return launch_narrow<D, FMT, 2>(c, a, ch, st);
+  if (ch.M == 16) return launch_narrow<D, FMT>(c, a, ch, st);
   return launch_wide<D, FMT>(a, ch, st);
 }
 
@@ -379,6 +375,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
     a.phase = fa::kKvWhole;
     a.M = l.whole.M;
     a.G = l.whole.G;
+    a.item_cost = l.whole.item_cost;
     a.part_o = reinterpret_cast<float*>(ws + l.pw.o);
     a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
     a.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pw.cuts);
@@ -389,6 +386,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   pf.phase = fa::kKvPrefix;
   pf.M = l.prefix.M;
   pf.G = l.prefix.G;
+  pf.item_cost = l.prefix.item_cost;
   pf.part_o = reinterpret_cast<float*>(ws + l.pp.o);
   pf.part_lse = reinterpret_cast<float*>(ws + l.pp.lse);
   pf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pp.cuts);
@@ -397,6 +395,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   sf.phase = fa::kKvSuffix;
   sf.M = l.suffix.M;
   sf.G = l.suffix.G;
+  sf.item_cost = l.suffix.item_cost;
   sf.part_o = reinterpret_cast<float*>(ws + l.ps.o);
   sf.part_lse = reinterpret_cast<float*>(ws + l.ps.lse);
   sf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.ps.cuts);

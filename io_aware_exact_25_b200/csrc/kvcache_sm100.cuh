@@ -47,6 +47,7 @@ struct KvArgs {
   int causal;
   float scale_log2;  // scale * log2(e)
   int M, G;          // rows of an item tile; CTAs of the launch
+  int item_cost;     // what starting and ending an item takes, in units of work
   int prefix_len;    // keys [0, prefix_len) are the batch's shared prefix (0: none)
   int phase;         // kKvWhole: all keys; kKvPrefix: the shared ones; kKvSuffix: the rest
   // pieces of items that several CTAs share: slot 2 c + s of CTA c
@@ -312,6 +313,10 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvArgs a) {
 // sequence by sequence, head by head, tile by tile, form one line that the G
 // CTAs of the grid cut into equal stretches, whatever the lengths: the cut is
 // computed on the device from the lengths, so a captured launch follows them.
+// Each item counts item_cost units more than its keys, ahead of them, for what
+// starting and ending it takes: without them the CTAs with many short items
+// were the last (64 sequences of 512 to 8192 keys, 8 key heads: 108 us for the
+// CTAs of one item, 2.7 us more for each further one, 132 us for those of ten).
 // An item inside one stretch is finished by its CTA; an item that is cut
 // leaves a normalised piece and its logsumexp per CTA, merged afterwards.  A
 // CTA has at most two such pieces, of its first and of its last item.
@@ -352,30 +357,54 @@ __device__ __forceinline__ int kv_end(const KvArgs& a, const KvSeq& s, int i) {
 
 __device__ __forceinline__ int kv_begin(const KvArgs& a) { return a.phase == kKvSuffix ? a.prefix_len : 0; }
 
+// In the functions below ONE says that every sequence's rows fit in one tile (the narrow kernel): most of the
+// arithmetic, divisions above all, then falls away, and with it a good part of a short call's time.
+
 // one past the last key that some row of tile rt sees
+template <bool ONE>
 __device__ __forceinline__ int kv_item_end(const KvArgs& a, const KvSeq& s, int rt) {
+  if (ONE) return kv_end(a, s, s.lq - 1);
   // rows of a call are fewer than 2^31, so row numbers stay 32-bit
   const uint32_t last = min((uint32_t)(rt + 1) * (uint32_t)a.M, (uint32_t)s.lq * (uint32_t)a.g) - 1u;
   return kv_end(a, s, (int)(last / (uint32_t)a.g));
 }
 
+template <bool ONE>
 __device__ __forceinline__ int kv_tiles(const KvArgs& a, const KvSeq& s) {
+  if (ONE) return s.lq > 0 ? 1 : 0;
   return (int)(((uint32_t)s.lq * (uint32_t)a.g + (uint32_t)a.M - 1u) / (uint32_t)a.M);
 }
 
+template <bool ONE>
 __device__ __forceinline__ int kv_item_units(const KvArgs& a, const KvSeq& s, int rt) {
-  const int keys = kv_item_end(a, s, rt) - kv_begin(a);
+  const int keys = kv_item_end<ONE>(a, s, rt) - kv_begin(a);
   return max(1, (keys + kKvUnit - 1) / kKvUnit);  // an item without keys still writes its rows
 }
 
-// units of one key head of the sequence
-__device__ __forceinline__ long long kv_head_units(const KvArgs& a, const KvSeq& s) {
-  const int nt = kv_tiles(a, s);
-  if (nt == 0) return 0;
-  if (nt == 1 || !a.causal || a.phase == kKvPrefix) return (long long)nt * kv_item_units(a, s, nt - 1);
+// length on the line of one key head of the sequence
+template <bool ONE>
+__device__ __forceinline__ long long kv_head_len(const KvArgs& a, const KvSeq& s) {
+  if (s.lq == 0) return 0;
+  if (ONE) return kv_item_units<true>(a, s, 0) + a.item_cost;
+  const int nt = kv_tiles<false>(a, s);
+  if (nt == 1 || !a.causal || a.phase == kKvPrefix)
+    return (long long)nt * (kv_item_units<false>(a, s, nt - 1) + a.item_cost);
   long long n = 0;
-  for (int rt = 0; rt < nt; ++rt) n += kv_item_units(a, s, rt);
+#pragma unroll 1
+  for (int rt = 0; rt < nt; ++rt) n += kv_item_units<false>(a, s, rt) + a.item_cost;
   return n;
+}
+
+// What a CTA with `left` of its stretch to go does of an item of n_item units from place `from` of the item on: units
+// [start, start + n), which take `take` of the line.  n = 0: its stretch ends before the item's first unit.
+struct KvPart {
+  int start, n, take;
+};
+
+__device__ __forceinline__ KvPart kv_part(const KvArgs& a, int n_item, int from, int left) {
+  const int take = min(n_item + a.item_cost - from, left);
+  const int start = max(from - a.item_cost, 0);
+  return KvPart{start, max(from + take - a.item_cost, 0) - start, take};
 }
 
 __device__ __forceinline__ int kv_num_seqs(const KvArgs& a) { return a.phase == kKvPrefix ? 1 : a.B; }
@@ -392,15 +421,17 @@ struct KvLine {
   }
 };
 
-// A place on the line of units: unit `unit` of row tile rt of head h of sequence b.
+// A place on the line: place `from` of the item that is row tile rt of head h of sequence b.
 struct KvPlace {
-  int b, h, rt, unit;
+  int b, h, rt, from;
 };
 
 // Scratch of kv_place.
 struct KvScan {
   long long warp_sum[32];
-  long long place[2];
+  long long rem;
+  int b;
+  KvSeq s;
 };
 
 // Inclusive sum over the block (NT threads) and its total.
@@ -426,80 +457,93 @@ __device__ __forceinline__ long long kv_block_inclusive(long long x, KvScan* sc,
   return before + x;
 }
 
-// The line of work, and the sequence that holds the first unit of CTA c (and the units before it within the
-// sequence), by the whole block; *b < 0 if CTA c has no stretch.
-template <int NT>
-__device__ __forceinline__ KvLine kv_place(const KvArgs& a, int c, int G, KvScan* sc, int* b, long long* rem) {
+// The line of work, and the sequence *s = number *b that holds the first unit of CTA c (and the units before it
+// within the sequence), by the whole block; *b < 0 if CTA c has no stretch.
+template <bool ONE, int NT>
+__device__ __forceinline__ KvLine kv_place(const KvArgs& a, int c, int G, KvScan* sc, int* b, KvSeq* s,
+                                           long long* rem) {
   const int n = kv_num_seqs(a);
+  KvSeq mine{0, 0, 0};
   auto units_of = [&](int i, bool report) -> long long {
     if (i >= n) return 0;
-    const KvSeq s = kv_seq(a, i, report);
-    return kv_head_units(a, s) * a.Hkv;
+    mine = kv_seq(a, i, report);
+    return kv_head_len<ONE>(a, mine) * a.Hkv;
   };
-  const long long mine = units_of((int)threadIdx.x, c == 0);  // the first NT sequences' units stay in registers
-  long long part = 0, incl = kv_block_inclusive<NT>(mine, sc, &part);
-  long long W = part;
-  if (n > NT) {
-    long long sum = 0, rest;
-    for (int i = NT + threadIdx.x; i < n; i += NT) sum += units_of(i, c == 0);
-    (void)kv_block_inclusive<NT>(sum, sc, &rest);
-    W += rest;
-  }
-  KvLine line{0, 0, (int)min((long long)G, W)};
+  KvLine line{0, 0, 0};
   *b = -1;
   *rem = 0;
-  if (W == 0) return line;
-  line.q = kv_div(W, line.G);
-  line.r = (int)(W - line.q * line.G);
-  if (c >= line.G) return line;
-  const long long u0 = line.cut(c);
-  long long run = 0, x = mine, tot = part;
-  for (int base = 0;;) {
-    const long long lo = run + incl - x;
-    if (u0 >= lo && u0 < lo + x) {
-      sc->place[0] = base + threadIdx.x;
-      sc->place[1] = u0 - lo;
+  long long W = 0, u0 = 0, run = 0, x = 0, incl = 0, tot = 0;
+  // first the sum of all sequences' units, then the one that holds this CTA's first (one body for both, so that the
+  // kernel's cold start fetches its instructions once; up to NT sequences stay in registers)
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int base = 0; base < n; base += NT) {
+      if (pass == 0 || n > NT) {
+        x = units_of(base + (int)threadIdx.x, pass == 0 && c == 0);
+        incl = kv_block_inclusive<NT>(x, sc, &tot);
+      }
+      if (pass == 0) {
+        W += tot;
+        continue;
+      }
+      const long long lo = run + incl - x;
+      if (u0 >= lo && u0 < lo + x) {
+        sc->b = base + threadIdx.x;
+        sc->rem = u0 - lo;
+        sc->s = mine;
+      }
+      run += tot;
+      if (u0 < run) break;
     }
-    if (u0 < run + tot) break;
-    run += tot;
-    base += NT;
-    x = units_of(base + threadIdx.x, false);
-    incl = kv_block_inclusive<NT>(x, sc, &tot);
+    if (pass == 0) {
+      line.G = (int)min((long long)G, W);
+      if (W == 0) return line;
+      line.q = kv_div(W, line.G);
+      line.r = (int)(W - line.q * line.G);
+      if (c >= line.G) return line;
+      u0 = line.cut(c);
+    }
   }
   __syncthreads();
-  *b = (int)sc->place[0];
-  *rem = sc->place[1];
+  *b = sc->b;
+  *rem = sc->rem;
+  *s = sc->s;
   return line;
 }
 
 // The place `rem` units into sequence b.
+template <bool ONE>
 __device__ __forceinline__ KvPlace kv_within(const KvArgs& a, const KvSeq& s, int b, long long rem) {
   KvPlace p;
   p.b = b;
-  const long long per = kv_head_units(a, s);
+  const long long per = kv_head_len<ONE>(a, s);
   p.h = (int)kv_div(rem, per);
   rem -= p.h * per;
   p.rt = 0;
-  const int nt = kv_tiles(a, s);
+  p.from = (int)rem;
+  if (ONE) return p;
+  const int nt = kv_tiles<false>(a, s);
   if (nt > 1 && (!a.causal || a.phase == kKvPrefix)) {
-    const int n = kv_item_units(a, s, 0);
+    const int n = kv_item_units<false>(a, s, 0) + a.item_cost;
     p.rt = (int)kv_div(rem, n);
     rem -= (long long)p.rt * n;
   } else {
     for (; p.rt + 1 < nt; ++p.rt) {
-      const int n = kv_item_units(a, s, p.rt);
+      const int n = kv_item_units<false>(a, s, p.rt) + a.item_cost;
       if (rem < n) break;
       rem -= n;
     }
   }
-  p.unit = (int)rem;
+  p.from = (int)rem;
   return p;
 }
 
 // The item after p; false at the end of the line.  Updates s when the sequence changes.
+template <bool ONE>
 __device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
-  p.unit = 0;
-  if (++p.rt < kv_tiles(a, s)) return true;
+  p.from = 0;
+  if (!ONE && ++p.rt < kv_tiles<false>(a, s)) return true;
   p.rt = 0;
   if (++p.h < a.Hkv) return true;
   p.h = 0;
@@ -511,19 +555,20 @@ __device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
   return false;
 }
 
-// Entry of the item at p (of n units, the first of them unit u, in CTA c's stretch) in the phases other than kKvWhole.
+// Entry of an item in the phases other than kKvWhole.
 __device__ __forceinline__ long long kv_item_index(const KvArgs& a, int b, int h, int rt) {
   const uint32_t rows = (uint32_t)(a.phase == kKvPrefix ? a.total : a.max_q) * (uint32_t)a.g;
   const uint32_t tiles = (rows + (uint32_t)a.M - 1u) / (uint32_t)a.M;  // of the longest sequence
   return ((long long)b * a.Hkv + h) * tiles + rt;
 }
 
-// Record where the item's pieces are; called by one thread of the CTA that starts the item.
-__device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvPlace& p, int c, long long u,
+// Record where the pieces of the item that starts at w0 of the line are; called by one thread of CTA c, which does its
+// first unit (as the first item of its stretch, or a later one).
+__device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvPlace& p, int c, long long w0,
                                           int n_item, bool whole, bool first_item) {
   if (whole && a.phase == kKvWhole) return;
   KvCut k;
-  k.n = whole ? 1 : line.cta_of(u + n_item - 1) - c + 1;
+  k.n = whole ? 1 : line.cta_of(w0 + a.item_cost + n_item - 1) - c + 1;
   k.first = 2 * c + (first_item ? 0 : 1);
   k.next = 2 * c + 2;
   k.b = p.b, k.h = p.h, k.rt = p.rt;

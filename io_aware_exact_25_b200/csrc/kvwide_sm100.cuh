@@ -30,7 +30,7 @@
 // largest scale).  A V scale that is NaN would spoil rows that do not see its
 // key, 0 x NaN: its row enters as zeros, and the rows that see it are made NaN
 // at the end, from a bit set of such keys per tile.  q goes into f16 as it is
-// if the row's largest entry is in [2^-2, 2^15), and shifted by a power of two
+// if the row's largest entry is in [2^-1, 2^15), and shifted by a power of two
 // that its scores take back otherwise.
 //
 // The scores of a row stay in its thread's registers: x = s ks - (m - 7) at
@@ -54,14 +54,16 @@ struct KvWideLayout {
   static_assert(256 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsCtl <= 128 * kThreads, "register split");
   static constexpr uint32_t kHalf = 128u * 128u;    // 128 rows x 64 f16 columns
   static constexpr uint32_t kTile = 128u * D * 2u;  // 128 x D f16
-  static constexpr int kStages = D == 128 ? 3 : 5;  // K/V operand ring
-  static constexpr int kRaw = D == 128 ? 3 : 5;     // ring of codes: K(j), V(j), K(j + 1), ...
+  // K/V operand ring.  Four tiles: K(j + 1) then takes the place of K(j - 1), which the step before freed; with three
+  // it took V(j - 1)'s, freed at the end of step j, and its conversion stood in the way (1200 clocks of 4100 a tile).
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kRaw = D == 128 ? 2 : 4;  // ring of codes: K(j), V(j), K(j + 1), ...
   static constexpr uint32_t kRawCodes = 128u * D;
-  static constexpr uint32_t kRawBytes = kRawCodes + 1024u;  // then 128 K scales and 128 V scales (K's slots only)
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = 2 * kTile;
   static constexpr uint32_t kOffRaw = kOffKV + kStages * kTile;
-  static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawBytes;  // [2] 128 K scales times the softmax scale
+  static constexpr uint32_t kOffRawScale = kOffRaw + kRaw * kRawCodes;  // [kRaw / 2] 128 K scales, 128 V scales
+  static constexpr uint32_t kOffScale = kOffRawScale + kRaw / 2 * 1024;  // [2] 128 K scales times the softmax scale
   static constexpr uint32_t kOffMisc = kOffScale + 2 * 512;        // [2] {V power, -, -, -, NaN keys [4]}, [2][4] maxima
   static constexpr uint32_t kOffBar = kOffMisc + 2 * 32 + 2 * 16;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kRaw + 2 + 4 + 2 + 2 + 2 + 1 + 1;
@@ -191,8 +193,9 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
   pdl_trigger();
   int b;
   long long rem;
-  const KvLine line =
-      kv_place<L::kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &rem);
+  KvSeq s{0, 0, 0};
+  const KvLine line = kv_place<false, L::kThreads>(a, blockIdx.x, gridDim.x,
+                                                   reinterpret_cast<KvScan*>(smem + L::kOffScan), &b, &s, &rem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -204,12 +207,8 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
   KvLine* s_line = reinterpret_cast<KvLine*>(smem + L::kOffScan);  // kept for kv_record only (the scan is over)
   if (threadIdx.x == 0) *s_line = line;
   const int begin = kv_begin(a);
-  KvSeq s{0, 0, 0};
   KvPlace at{0, 0, 0, 0};
-  if (run) {
-    s = kv_seq(a, b, false);
-    at = kv_within(a, s, b, rem);
-  }
+  if (run) at = kv_within<false>(a, s, b, rem);
   // Every role walks the same items: n units of the item at `at`, from key `first` on; act1 if the second row tile
   // has rows.
   auto act1_of = [&]() { return (uint32_t)at.rt * 256u + 128u < (uint32_t)s.lq * (uint32_t)a.g; };
@@ -264,7 +263,9 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
         return true;
       };
       for (int left = total; left > 0 && ok;) {
-        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
+        const KvPart part = kv_part(a, kv_item_units<false>(a, s, at.rt), at.from, left);
+        const int n = part.n;
+        if (n == 0) break;  // the stretch ends before the item's first unit
         const int nt = act1_of() ? 2 : 1;
 #pragma unroll 1
         for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_warp(&bar_q[t], (t ? nq1++ : nq0++) & 1u, ab);
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
           if (j < n) mma_commit_elect(&bar_kv_empty[pk % L::kStages]);
         }
         pos += 2u * n;
-        left -= n;
-        if (left > 0 && !kv_next(a, s, at)) break;
+        left -= part.take;
+        if (left > 0 && !kv_next<false>(a, s, at)) break;
       }
       if (issued) {
         mma_commit_elect(bar_drain);
@@ -302,9 +303,11 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
       uint32_t pos = 0;
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
-        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
-        const int item_end = kv_item_end(a, s, at.rt);
-        const int first = begin + at.unit * kKvUnit;
+        const KvPart part = kv_part(a, kv_item_units<false>(a, s, at.rt), at.from, left);
+        const int n = part.n;
+        if (n == 0) break;  // the stretch ends before the item's first unit
+        const int item_end = kv_item_end<false>(a, s, at.rt);
+        const int first = begin + part.start * kKvUnit;
         const int* trow = a.table + (a.phase == kKvPrefix ? 0ll : at.b * a.table_stride);
         auto fetch = [&](int j) -> int {  // this lane's cache row in tile j, or -1
           const int key = first + j * kKvUnit + g * lane;
@@ -330,19 +333,20 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
             if (!(ok = mbar_wait_warp(&bar_raw_empty[sl], ((pos / L::kRaw) & 1u) ^ 1u, ab))) break;
             if (lane == 0) mbar_arrive_expect_tx(&bar_raw_full[sl], rows * (uint32_t)(which ? D : D + 8));
             __syncwarp();
-            uint8_t* dst = smem + L::kOffRaw + sl * L::kRawBytes;
+            uint8_t* dst = smem + L::kOffRaw + sl * L::kRawCodes;
+            uint8_t* dst_sc = smem + L::kOffRawScale + (sl >> 1) * 1024;
             if (in) {
               bulk_load(dst + g * lane * D, (which ? a.v : a.k) + row * D, (uint32_t)(g * D), &bar_raw_full[sl]);
               if (which == 0) {
-                bulk_load(dst + L::kRawCodes + 4 * g * lane, a.ks + row, 4u * g, &bar_raw_full[sl]);
-                bulk_load(dst + L::kRawCodes + 512 + 4 * g * lane, a.vs + row, 4u * g, &bar_raw_full[sl]);
+                bulk_load(dst_sc + 4 * g * lane, a.ks + row, 4u * g, &bar_raw_full[sl]);
+                bulk_load(dst_sc + 512 + 4 * g * lane, a.vs + row, 4u * g, &bar_raw_full[sl]);
               }
             }
             ++pos;
           }
         }
-        left -= n;
-        if (left > 0 && !kv_next(a, s, at)) break;
+        left -= part.take;
+        if (left > 0 && !kv_next<false>(a, s, at)) break;
       }
       // every copy asked for lands before the CTA may exit
       for (uint32_t p = pos > L::kRaw ? pos - L::kRaw : 0u; p < pos; ++p)
@@ -367,14 +371,16 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
       uint32_t pos = 0, nsc = 0;
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
-        const int n = min(kv_item_units(a, s, at.rt) - at.unit, left);
-        const int item_end = kv_item_end(a, s, at.rt);
-        const int first = begin + at.unit * kKvUnit;
+        const KvPart part = kv_part(a, kv_item_units<false>(a, s, at.rt), at.from, left);
+        const int n = part.n;
+        if (n == 0) break;  // the stretch ends before the item's first unit
+        const int item_end = kv_item_end<false>(a, s, at.rt);
+        const int first = begin + part.start * kKvUnit;
         float vpower = 1.1754943508222875e-38f;
         // the next tile of codes, converted; rows' factors if it is V's
         auto convert = [&](const uint32_t* ratio) -> bool {
           const uint32_t st = pos % L::kStages, sl = pos % L::kRaw;
-          const uint32_t src = sbase + L::kOffRaw + sl * L::kRawBytes + ch * 16;
+          const uint32_t src = sbase + L::kOffRaw + sl * L::kRawCodes + ch * 16;
           if (ratio && !mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab)) return false;
           uint4 raw[NP];
 #pragma unroll
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
         for (int j = 0; j < n; ++j) {
           const uint32_t sl = pos % L::kRaw;
           if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
-          const uint32_t raw_sc = sbase + L::kOffRaw + sl * L::kRawBytes + L::kRawCodes;
+          const uint32_t raw_sc = sbase + L::kOffRawScale + (sl >> 1) * 1024;
           const int key0 = first + j * kKvUnit;
           const bool in = key0 + tid < item_end;
           const float ks = in ? ld_shared_f(raw_sc + 4 * tid) : 0.f;
@@ -459,8 +465,8 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
           if (!(ok = convert(nullptr))) break;
           if (!(ok = convert(ratio))) break;
         }
-        left -= n;
-        if (left > 0 && !kv_next(a, s, at)) break;
+        left -= part.take;
+        if (left > 0 && !kv_next<false>(a, s, at)) break;
       }
     }
   } else {
@@ -475,9 +481,11 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
       uint32_t ns = 0, nsc = 0;  // score tiles and scale stages so far
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
-        const int n_item = kv_item_units(a, s, at.rt);
-        const int n = min(n_item - at.unit, left);
-        const int first = begin + at.unit * kKvUnit;
+        const int n_item = kv_item_units<false>(a, s, at.rt);
+        const KvPart part = kv_part(a, n_item, at.from, left);
+        const int n = part.n;
+        if (n == 0) break;
+        const int first = begin + part.start * kKvUnit;
         if (t == 1 && !act1_of()) {
           // no rows here: only release the scales
           for (int j = 0; j < n && ok; ++j, ++nsc) {
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
                                          __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu)));
             const float amax = __uint_as_float(max(m2 & 0xffffu, m2 >> 16) << 16);
             float down = 1.f;
-            if (!(amax == 0.f || (amax >= 0.25f && amax < 32768.f))) kv_q_shift(amax, down, up);
+            if (!(amax == 0.f || (amax >= 0.5f && amax < 32768.f))) kv_q_shift(amax, down, up);
             const uint32_t row = sbase + L::kOffQ + t * L::kTile + r * 128;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
@@ -648,9 +656,10 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
           if (ok) ok = mbar_wait_warp(&bar_pv[t], (ns - 1) & 1u, ab);
           if (ok) {
             tc_fence_after();
-            const bool whole = at.unit == 0 && n == n_item;
-            if (at.unit == 0 && threadIdx.x == 0)
-              kv_record(a, *s_line, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left), n_item, whole, left == total);
+            const bool whole = n == n_item;
+            if (part.start == 0 && threadIdx.x == 0)
+              kv_record(a, *s_line, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left) - at.from, n_item, whole,
+                        left == total);
             const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + t * 128 + r;
             float f = l == 0.f ? 0.f : vpower * (kv_code_scale<FMT>() / kv_v_shift<FMT>()) / l;
             if (spoiled) f = __uint_as_float(0x7fc00000u);
@@ -668,8 +677,8 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
             tc_fence_before();
           }
         }
-        left -= n;
-        if (left > 0 && !kv_next(a, s, at)) break;
+        left -= part.take;
+        if (left > 0 && !kv_next<false>(a, s, at)) break;
       }
     }
   }

@@ -460,14 +460,14 @@ def test_shared_prefix_of_one_sequence_and_untouched_rows():
     x = Batch(INT8, 128, 16, 2, 4, q=[1], lens=[100], prefix=64, seed=13)
     assert torch.equal(x.run()[0], x.run(prefix=0)[0])
     x = Batch(FP8, 64, 16, 2, 4, q=[1, 2], lens=[100, 90], prefix=64, seed=14)
-    o, lse = x.run()
+    x.check(*x.run())
     out = torch.full((6, 8, 64), 5.0, device="cuda").to(torch.bfloat16)
     l2 = torch.full((8, 6), 3.0, device="cuda")
     q = torch.zeros((6, 8, 64), device="cuda").to(torch.bfloat16)
     q[1:4] = x.q
     binding.fwd_kvcache(q, x.cache._abi, x.cache._tensors, x.table_dev, x.seqlens, 2, cu_seqlens_q=x.cu + 1, o=out,
                         lse=l2, prefix_len=64)
-    assert torch.equal(out[1:4], o) and torch.equal(l2[:, 1:4], lse)
+    x.check(out[1:4], l2[:, 1:4])  # (not to the bit: 24 rows may take another kernel than 12)
     assert (out[0] == 5).all() and (out[4:] == 5).all() and (l2[:, 0] == 3).all() and (l2[:, 4:] == 3).all()
 
 
