@@ -544,76 +544,80 @@ def bwd_finalize(dq, workspace, scale, stream=None):
     return dq
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+class KvBuffers:
+    """A quantised, paged cache's four buffers, checked once, and their C-ABI view: codes ``k``, ``v`` [num_pages,
+    num_kv_heads, page_size, d] int8 or float8_e4m3fn and fp32 ``k_scale``, ``v_scale`` [num_pages, num_kv_heads,
+    page_size], dense CUDA tensors of one device."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
+            if t.device != k.device:
+                raise ValueError("the cache's tensors must be on one device")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if k.dtype not in KV_FORMATS or v.dtype != k.dtype:
+            raise ValueError("k and v must both be int8 or both float8_e4m3fn")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [num_pages, num_kv_heads, page_size, d] of one shape")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("k_scale and v_scale must be float32")
+        if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+            raise ValueError("k_scale and v_scale must be [num_pages, num_kv_heads, page_size]")
+        P, H, ps, d = k.shape
+        if ps not in (16, 32, 64, 128):
+            raise ValueError("page_size is 16, 32, 64 or 128")
+        if d not in (64, 128):
+            raise ValueError("head_dim is 64 or 128")
+        self.tensors = (k, v, k_scale, v_scale)  # the view below holds addresses only
+        self.num_pages, self.num_kv_heads, self.page_size, self.d = P, H, ps, d
+        self.device, self.index = k.device, k.device.index
+        self.abi = FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, ps, H, d,
+                             KV_FORMATS[k.dtype])
+        self.ref = ctypes.byref(self.abi)
 
 
-def _on(device, stream):
-    """(context, stream handle) for a call on tensors of ``device``: inside the context that device and the given
-    stream are current, so that what is allocated there belongs to them."""
+def _other_stream(c, stream):
+    """None if the call goes to the current stream of the current device, which is the cache's; else a context inside
+    which the cache's device and the given stream (None: the device's current one) are current, so that what is
+    allocated or copied there belongs to them."""
     if stream is None:
-        index = device.index
-        if index == torch.cuda.current_device():
-            return _NO_CONTEXT, torch._C._cuda_getCurrentRawStream(index)
-        return torch.cuda.device(device), torch._C._cuda_getCurrentRawStream(index)
+        return None if torch.cuda.current_device() == c.index else torch.cuda.device(c.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.device != device:
+        stream = torch.cuda.ExternalStream(int(stream), device=c.device)
+    if stream.device != c.device:
         raise ValueError("stream must belong to the tensors' device")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    return torch.cuda.stream(stream)
 
 
-def kv_cache(k, v, k_scale, v_scale) -> FaKvCache:
-    """The C-ABI view of a cache's buffers: codes ``k``, ``v`` [num_pages, num_kv_heads, page_size, d] int8 or
-    float8_e4m3fn and fp32 ``k_scale``, ``v_scale`` [num_pages, num_kv_heads, page_size], dense CUDA tensors.  It holds
-    addresses only; the tensors must outlive it."""
-    for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors (there is no CPU path)")
-        if t.device != k.device:
-            raise ValueError("the cache's tensors must be on one device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if k.dtype not in KV_FORMATS or v.dtype != k.dtype:
-        raise ValueError("k and v must both be int8 or both float8_e4m3fn")
-    if k.dim() != 4 or v.shape != k.shape:
-        raise ValueError("k and v must be [num_pages, num_kv_heads, page_size, d] of one shape")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
-        raise ValueError("k_scale and v_scale must be float32")
-    if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
-        raise ValueError("k_scale and v_scale must be [num_pages, num_kv_heads, page_size]")
-    P, H, ps, d = k.shape
-    return FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, ps, H, d,
-                     KV_FORMATS[k.dtype])
+def _check_ints(name, t, c, n):
+    """A dense int32 vector of n entries on the cache's device."""
+    if t.dtype != torch.int32 or t.shape != (n,) or t.device != c.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on the cache's device")
 
 
-def _check_ints(name, t, device, n=None):
-    """A dense int32 vector (of n entries) on the cache's device."""
-    if t.device != device or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries")
-
-
-def _check_table(block_table, device):
-    """int32 [B, max_pages] on the cache's device, rows dense and apart."""
-    t = block_table
-    if t.device != device or t.dtype != torch.int32 or t.dim() != 2:
+def _check_table(t, c):
+    """int32 [B, max_pages] on the cache's device, rows dense and apart; returns B, max_pages and the row stride."""
+    if t.dtype != torch.int32 or t.dim() != 2 or t.device != c.device:
         raise ValueError("block_table must be an int32 [B, max_pages] tensor on the cache's device")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    B, pages = t.shape
+    row, col = t.stride()
+    if pages > 1 and col != 1:
         raise ValueError("the rows of block_table must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if B > 1 and row < pages:
         raise ValueError("the rows of block_table must not overlap")
-    return t.shape
+    return B, pages, row
 
 
-def _check_tokens(name, t, shape, device):
+def _check_tokens(name, t, shape, c):
     """bf16 tensor of the given shape on the cache's device."""
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on the cache's device (there is no CPU path)")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be bf16")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != c.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the cache's device (there is no CPU path)")
 
 
 def _rows_usable(t) -> bool:
@@ -632,98 +636,107 @@ def _pair_strides(a, b):
     return _SixInts(0, a1, a0, 0, b1, b0)
 
 
-def _kv_rows(fn, what, cache, tensors, k, v, block_table, starts, cu_seqlens, stream):
-    device = tensors[0].device
-    B, max_pages = _check_table(block_table, device)
+def kv_append(c: KvBuffers, k, v, block_table, starts=None, cu_seqlens=None, stream=None):
+    """Quantise bf16 ``k``, ``v`` [T, num_kv_heads, d] into a cache via ``fa_kv_append``."""
+    ctx = _other_stream(c, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_append(c, k, v, block_table, starts, cu_seqlens)
     T = k.shape[0]
+    _check_tokens("k", k, (T, c.num_kv_heads, c.d), c)
+    _check_tokens("v", v, (T, c.num_kv_heads, c.d), c)
+    if not _rows_usable(k):
+        k = k.contiguous()
+    if not _rows_usable(v):
+        v = v.contiguous()
+    _kv_rows(load().fa_kv_append, "fa_kv_append", c, k, v, T, block_table, starts, cu_seqlens)
+
+
+def kv_read(c: KvBuffers, block_table, total_tokens, starts=None, cu_seqlens=None, k=None, v=None, stream=None):
+    """bf16 k, v [total_tokens, num_kv_heads, d] of a cache's positions via ``fa_kv_read``."""
+    ctx = _other_stream(c, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_read(c, block_table, total_tokens, starts, cu_seqlens, k, v)
+    shape = (int(total_tokens), c.num_kv_heads, c.d)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+    else:
+        _check_tokens("k", k, shape, c)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+    else:
+        _check_tokens("v", v, shape, c)
+    _kv_rows(load().fa_kv_read, "fa_kv_read", c, k, v, shape[0], block_table, starts, cu_seqlens)
+    return k, v
+
+
+def _kv_rows(fn, what, c, k, v, T, block_table, starts, cu_seqlens):
+    B, max_pages, row = _check_table(block_table, c)
     if starts is not None:
-        _check_ints("starts", starts, device, B)
+        _check_ints("starts", starts, c, B)
     if cu_seqlens is not None:
-        _check_ints("cu_seqlens", cu_seqlens, device, B + 1)
+        _check_ints("cu_seqlens", cu_seqlens, c, B + 1)
     elif T != B:
         raise ValueError("without cu_seqlens there is one token per sequence")
-    ctx, s = _on(device, stream)
-    with ctx:
-        if fn.__name__ == "fa_kv_append":  # inputs of other layouts are copied once, on the call's stream
-            k, v = (t if _rows_usable(t) else t.contiguous() for t in (k, v))
-        _call(fn(ctypes.byref(cache), _ptr(k), _ptr(v), _pair_strides(k, v), _ptr(block_table), max_pages,
-                 block_table.stride(0), _ptr(starts), _ptr(cu_seqlens), B, T, s), what)
-
-
-def kv_append(cache, tensors, k, v, block_table, starts=None, cu_seqlens=None, stream=None):
-    """Quantise bf16 ``k``, ``v`` [T, num_kv_heads, d] into a cache (``kv_cache`` of ``tensors``, its four buffers) via
-    ``fa_kv_append``."""
-    P, H, ps, d = tensors[0].shape
-    if k.dim() != 3:
-        raise ValueError("k and v must be [T, num_kv_heads, d]")
-    _check_tokens("k", k, (k.shape[0], H, d), tensors[0].device)
-    _check_tokens("v", v, (k.shape[0], H, d), tensors[0].device)
-    _kv_rows(load().fa_kv_append, "fa_kv_append", cache, tensors, k, v, block_table, starts, cu_seqlens, stream)
-
-
-def kv_read(cache, tensors, block_table, total_tokens, starts=None, cu_seqlens=None, k=None, v=None, stream=None):
-    """bf16 k, v [total_tokens, num_kv_heads, d] of a cache's positions via ``fa_kv_read``."""
-    P, H, ps, d = tensors[0].shape
-    device = tensors[0].device
-    shape = (int(total_tokens), H, d)
-    ctx, s = _on(device, stream)
-    if k is None or v is None:
-        with ctx:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=device) if k is None else k
-            v = torch.empty(shape, dtype=torch.bfloat16, device=device) if v is None else v
-    _check_tokens("k", k, shape, device)
-    _check_tokens("v", v, shape, device)
-    _kv_rows(load().fa_kv_read, "fa_kv_read", cache, tensors, k, v, block_table, starts, cu_seqlens, stream)
-    return k, v
+    rc = fn(c.ref, k.data_ptr(), v.data_ptr(), _pair_strides(k, v), block_table.data_ptr(), max_pages, row,
+            _ptr(starts), _ptr(cu_seqlens), B, T, torch._C._cuda_getCurrentRawStream(c.index))
+    if rc != FA_OK:
+        raise FaError(rc, what)
 
 
 def fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len=0) -> int:
     return int(load().fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len))
 
 
-def fwd_kvcache(q, cache, tensors, block_table, seqlens, max_q, cu_seqlens_q=None, causal=True, scale=None,
-                prefix_len=0, o=None, lse=None, want_lse=True, workspace=None, stream=None):
+def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None, causal=True, scale=None, prefix_len=0,
+                o=None, lse=None, want_lse=True, workspace=None, stream=None):
     """O [T, Hq, d] and lse [Hq, T] (or None) of the newest tokens' attention over a cache via ``fa_fwd_kvcache``."""
-    P, Hkv, ps, d = tensors[0].shape
-    device = tensors[0].device
+    ctx = _other_stream(c, stream)
+    if ctx is not None:
+        with ctx:
+            return fwd_kvcache(q, c, block_table, seqlens, max_q, cu_seqlens_q, causal, scale, prefix_len, o, lse,
+                               want_lse, workspace)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, d]")
-    T, Hq, _ = q.shape
-    _check_tokens("q", q, (T, Hq, d), device)
+    T, Hq, d = q.shape
+    Hkv = c.num_kv_heads
+    _check_tokens("q", q, (T, Hq, c.d), c)
     if Hq % Hkv != 0:
         raise ValueError(f"the {Hq} query heads are not a multiple of the cache's {Hkv} heads")
-    B, max_pages = _check_table(block_table, device)
-    _check_ints("seqlens", seqlens, device, B)
+    B, max_pages, row = _check_table(block_table, c)
+    _check_ints("seqlens", seqlens, c, B)
     if cu_seqlens_q is not None:
-        _check_ints("cu_seqlens_q", cu_seqlens_q, device, B + 1)
+        _check_ints("cu_seqlens_q", cu_seqlens_q, c, B + 1)
     elif B * max_q != T:
         raise ValueError("without cu_seqlens_q every sequence has max_q queries")
-    if prefix_len % ps != 0 or not 0 <= prefix_len <= max_pages * ps:
+    if prefix_len and (prefix_len % c.page_size != 0 or not 0 <= prefix_len <= max_pages * c.page_size):
         raise ValueError("prefix_len must be a multiple of the page size within the block table")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    lib = load()
-    ctx, s = _on(device, stream)
-    with ctx:
-        if not _rows_usable(q):
-            q = q.contiguous()
-        if o is None:
-            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
-        else:
-            _check_tokens("o", o, (T, Hq, d), device)
-        if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if want_lse else None
-        elif lse.device != device or lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
+    if not _rows_usable(q):
+        q = q.contiguous()
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=c.device)
+    else:
+        _check_tokens("o", o, (T, Hq, d), c)
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (Hq, T) or lse.device != c.device or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on the cache's device")
-        if workspace is None:
-            need = lib.fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, T, max_q, prefix_len)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
+    elif want_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=c.device)
+    lib = load()
+    if workspace is None:
+        need = lib.fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, T, max_q, prefix_len)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
+    else:
+        if workspace.device != c.device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        _call(lib.fa_fwd_kvcache(_ptr(q), _ptr(o), _ptr(lse), _pair_strides(q, o), ctypes.byref(cache),
-                                 _ptr(block_table), max_pages, block_table.stride(0), _ptr(seqlens),
-                                 _ptr(cu_seqlens_q), B, Hq, T, max_q, float(scale), int(bool(causal)), prefix_len,
-                                 _ptr(workspace), workspace.numel() * workspace.element_size(), s), "fa_fwd_kvcache")
+        need = workspace.numel() * workspace.element_size()
+    rc = lib.fa_fwd_kvcache(q.data_ptr(), o.data_ptr(), _ptr(lse), _pair_strides(q, o), c.ref, block_table.data_ptr(),
+                            max_pages, row, seqlens.data_ptr(), _ptr(cu_seqlens_q), B, Hq, T, max_q,
+                            1.0 / math.sqrt(d) if scale is None else float(scale), 1 if causal else 0, prefix_len,
+                            workspace.data_ptr(), need, torch._C._cuda_getCurrentRawStream(c.index))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_kvcache")
     return o, lse
 
 

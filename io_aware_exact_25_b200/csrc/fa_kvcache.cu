@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -223,26 +224,40 @@ int launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t
   return e == cudaSuccess ? FA_OK : fa_host::cuda_fail(e);
 }
 
+// Allow a kernel its dynamic shared memory, once per device (the attribute stays with the device's context).
+template <auto kKernel>
+int allow_smem(size_t smem) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return FA_OK;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return FA_OK;
+}
+
 template <int D, int FMT>
 int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
   using L = Narrow<D>;
-  auto kern = fa::kv_narrow_kernel<D, FMT, L>;
+  constexpr auto kern = fa::kv_narrow_kernel<D, FMT, L>;
   CUtensorMap mk, mv;
   const int box = c->page_size < 32 ? c->page_size : 32;
   int rc;
   if ((rc = make_code_map(&mk, c->k, c, box)) != FA_OK) return rc;
   if ((rc = make_code_map(&mv, c->v, c, box)) != FA_OK) return rc;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
-  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  if ((rc = allow_smem<kern>(L::kSmem)) != FA_OK) return rc;
   return launch(kern, dim3(ch.G), 128, L::kSmem, st, a.phase == fa::kKvSuffix, mk, mv, a);
 }
 
 template <int D, int FMT>
 int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
   using L = fa::KvWideLayout<D>;
-  auto kern = fa::kv_wide_kernel<D, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
-  if (e != cudaSuccess) return fa_host::cuda_fail(e);
+  constexpr auto kern = fa::kv_wide_kernel<D, FMT>;
+  const int rc = allow_smem<kern>(L::kSmem);
+  if (rc != FA_OK) return rc;
   return launch(kern, dim3(ch.G), L::kThreads, L::kSmem, st, a.phase == fa::kKvSuffix, a);
 }
 

@@ -63,7 +63,9 @@ struct KvArgs {
 // item that c starts and does not finish (n = 0: none).  Other phases: the entry of an item; n = 1 is a finished item,
 // whose rows are in row_o and row_lse.
 struct KvCut {
-  int n, first, next, b, h, rt, pad[2];
+  int n, first, next, h, rt;
+  int row0, lq;  // the sequence's rows
+  int pad;
 };
 
 enum : int { kKvWhole = 0, kKvPrefix = 1, kKvSuffix = 2 };
@@ -115,11 +117,15 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // bits) or further than 2^-16 of its value away from one: with 8-bit integers
 // X, A and a border of M / 2^n, M < 2^8, |top X 2^i - M A| is a whole number of
 // units of which M A is at most 2^16.  y carries a relative error below 2^-21 (a
-// reciprocal good to an ulp, two rounded products), so this rounding puts every border
-// case exactly on its border and moves nothing across one: the code that
-// follows is the exact quotient's, half to even, without a division.
-__device__ __forceinline__ float kv_snap(float y) {
-  return __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+// reciprocal good to an ulp, two rounded products), so this rounding puts every
+// border case exactly on its border and moves nothing across one: the code that
+// follows is the exact quotient's, half to even, without a division.  The
+// rounding is Veltkamp's splitting, p = (2^4 + 1) y, (y - p) + p, on both halves
+// of a packed pair (integer operations on the bits are fewer, but go to the
+// pipe that bounds the kernel).
+__device__ __forceinline__ uint64_t kv_snap2(uint64_t y) {
+  const uint64_t p = f2_mul(y, f2_pack(17.f, 17.f));
+  return f2_add(f2_fma(p, f2_pack(-1.f, -1.f), y), p);
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -128,20 +134,24 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// The codes of two packed pairs of quotients.
 template <int FMT>
-__device__ __forceinline__ uint32_t kv_encode4(float y0, float y1, float y2, float y3) {
+__device__ __forceinline__ uint32_t kv_encode4(uint64_t y01, uint64_t y23) {
+  float a, b, c, d;
   if constexpr (FMT == kKvInt8) {
     // adding 1.5 * 2^23 rounds half to even and leaves the two's complement
     // of the whole number in the low byte
-    const uint32_t a = __float_as_uint(__fadd_rn(kv_snap(y0), 12582912.f));
-    const uint32_t b = __float_as_uint(__fadd_rn(kv_snap(y1), 12582912.f));
-    const uint32_t c = __float_as_uint(__fadd_rn(kv_snap(y2), 12582912.f));
-    const uint32_t d = __float_as_uint(__fadd_rn(kv_snap(y3), 12582912.f));
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    const uint64_t magic = f2_pack(12582912.f, 12582912.f);
+    f2_unpack(f2_add(kv_snap2(y01), magic), a, b);
+    f2_unpack(f2_add(kv_snap2(y23), magic), c, d);
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
   } else {
+    f2_unpack(kv_snap2(y01), a, b);
+    f2_unpack(kv_snap2(y23), c, d);
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(kv_snap(y1)), "f"(kv_snap(y0)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(kv_snap(y3)), "f"(kv_snap(y2)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   }
 }
@@ -181,6 +191,8 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   constexpr float kTop = FMT == kKvInt8 ? 127.f : 448.f;
+  constexpr uint32_t kTinyBits = (127u - 100u) << 7;  // 2^-100 as a bf16
+  static_assert(kKvUnroll % 2 == 0, "rows go through the shuffles in pairs");
   const int lane = threadIdx.x & 31;
   const int units = (2 * a.Hkv + kv_rows_per_unit<D>() - 1) / kv_rows_per_unit<D>();  // per token
   const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -208,51 +220,64 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
   if (t < first || t >= end) return;  // a row of no sequence
   const long long row = kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
   if (row < 0) return;
+  // the largest |x| of each row as bf16 bits -- as integers infinities and NaN sort above all numbers --, two rows to
+  // a word on their way through the shuffles
+  uint32_t mb[kKvUnroll];
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; ++u) {
+    const uint32_t m2 = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
+                                 __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+    mb[u] = max(m2 & 0xffffu, m2 >> 16);
+  }
+  bool tiny = false;  // some row's largest is below 2^-100
+#pragma unroll
+  for (int u = 0; u < kKvUnroll; u += 2) {
+    uint32_t m2 = mb[u] | (mb[u + 1] << 16);
+#pragma unroll
+    for (int s = 1; s < LPR; s <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, s));
+    mb[u] = m2 & 0xffffu;
+    mb[u + 1] = m2 >> 16;
+    tiny |= mb[u] < kTinyBits || mb[u + 1] < kTinyBits;
+  }
+  const bool lifted = __any_sync(0xffffffffu, tiny);
 #pragma unroll
   for (int u = 0; u < kKvUnroll; ++u) {
     const int r = r0 + u * RPW;
-    const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    // the largest |x| as bf16 bits: as integers infinities and NaN sort above all numbers
-    uint32_t m2 = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, xs[i] & 0x7fff7fffu);
-#pragma unroll
-    for (int s = 1; s < LPR; s <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, s));
-    const uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
-    const float amax = __uint_as_float(mb << 16);
-    const bool finite = mb < 0x7f80u;
+    const float amax = __uint_as_float(mb[u] << 16);
     // top / amax to an ulp or two (the codes ask for no more), and amax / top by one step of Newton's division on
-    // the rounded reciprocal of top: the residual fma is exact, so the quotient is correctly rounded
-    float lift = 1.f, inv = kTop * rcp_approx(amax);
+    // the rounded reciprocal of top: the residual fma is exact, so the quotient is correctly rounded.  A row with an
+    // infinity or a NaN gets a NaN scale; its codes mean nothing.
+    float inv = kTop * rcp_approx(amax);
     const float s0 = amax * (1.f / kTop);
     float scale = fmaf(fmaf(-kTop, s0, amax), 1.f / kTop, s0);
-    const bool tiny = amax < 7.888609052210118e-31f;  // below 2^-100: lifted by 2^100, so that nothing leaves the range
-    if (tiny) {
-      lift = 1.2676506002282294e30f;
-      inv = mb != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
-      scale = __fdiv_rn(amax, kTop);
-    }
-    const bool any_tiny = __any_sync(0xffffffffu, tiny);
-    uint32_t c[2];
+    if (mb[u] >= 0x7f80u) scale = __uint_as_float(0x7fc00000u);
+    const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+    uint64_t y[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float y[4] = {bf16_lo(xs[2 * i]), bf16_hi(xs[2 * i]), bf16_lo(xs[2 * i + 1]), bf16_hi(xs[2 * i + 1])};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (any_tiny) y[e] *= lift;
-        y[e] = finite ? y[e] * inv : 0.f;
+    for (int i = 0; i < 4; ++i) y[i] = f2_pack(bf16_lo(xs[i]), bf16_hi(xs[i]));
+    if (lifted) {
+      // rows below 2^-100 go up by 2^100, so that nothing leaves fp32's range; a row of zeros keeps scale 0
+      const bool t = mb[u] < kTinyBits;
+      const float lift = t ? 1.2676506002282294e30f : 1.f;
+      if (t) {
+        inv = mb[u] != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
+        scale = __fdiv_rn(amax, kTop);
       }
-      c[i] = kv_encode4<FMT>(y[0], y[1], y[2], y[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = f2_pack(bf16_lo(xs[i]) * lift, bf16_hi(xs[i]) * lift);
     }
+    const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = f2_mul(y[i], inv2);
+    const uint32_t c0 = kv_encode4<FMT>(y[0], y[1]), c1 = kv_encode4<FMT>(y[2], y[3]);
     if (r < 2 * a.Hkv) {
       const int h = r < a.Hkv ? r : r - a.Hkv;
       const long long at = row + ((long long)h << a.page_shift);
       const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
       (void)lim;
       if (FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
-        *reinterpret_cast<uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col) = make_uint2(c[0], c[1]);
-        if (lane % LPR == 0)
-          (r < a.Hkv ? a.ks : a.vs)[at] = finite ? scale : __uint_as_float(0x7fc00000u);
+        *reinterpret_cast<uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col) = make_uint2(c0, c1);
+        if (lane % LPR == 0) (r < a.Hkv ? a.ks : a.vs)[at] = scale;
       }
     }
   }
@@ -564,14 +589,16 @@ __device__ __forceinline__ long long kv_item_index(const KvArgs& a, int b, int h
 
 // Record where the pieces of the item that starts at w0 of the line are; called by one thread of CTA c, which does its
 // first unit (as the first item of its stretch, or a later one).
-__device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvPlace& p, int c, long long w0,
-                                          int n_item, bool whole, bool first_item) {
+__device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvSeq& s, const KvPlace& p, int c,
+                                          long long w0, int n_item, bool whole, bool first_item) {
   if (whole && a.phase == kKvWhole) return;
   KvCut k;
   k.n = whole ? 1 : line.cta_of(w0 + a.item_cost + n_item - 1) - c + 1;
   k.first = 2 * c + (first_item ? 0 : 1);
   k.next = 2 * c + 2;
-  k.b = p.b, k.h = p.h, k.rt = p.rt;
+  k.h = p.h, k.rt = p.rt;
+  k.row0 = s.row0, k.lq = s.lq;
+  k.pad = 0;
   a.cuts[a.phase == kKvWhole ? c : kv_item_index(a, p.b, p.h, p.rt)] = k;
 }
 
@@ -580,13 +607,17 @@ struct KvRow {
   int token, head, end;
 };
 
-__device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
-  KvRow x;
+__device__ __forceinline__ KvRow kv_token_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
   const uint32_t rr = (uint32_t)rt * (uint32_t)a.M + (uint32_t)r;
   if (rr >= (uint32_t)s.lq * (uint32_t)a.g) return KvRow{-1, 0, 0};
   const int i = (int)(rr / (uint32_t)a.g);
-  x.token = s.row0 + i;
-  x.head = h * a.g + (int)(rr - (uint32_t)i * (uint32_t)a.g);
+  return KvRow{s.row0 + i, h * a.g + (int)(rr - (uint32_t)i * (uint32_t)a.g), 0};
+}
+
+__device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
+  KvRow x = kv_token_of(a, s, h, rt, r);
+  if (x.token < 0) return x;
+  const int i = x.token - s.row0;
   x.end = kv_end(a, s, i);
   if (a.phase == kKvPrefix) {
     // the token's own sequence bounds what it sees of the prefix
@@ -717,20 +748,38 @@ __device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces& p0
   const int me = group == 1 ? 0 : warp;
   const int n = p0.n + p1.n;
   auto lse_of = [&](int k) { return k < p0.n ? p0.lse[p0.at(k)] : p1.lse[p1.at(k - p0.n)]; };
-  // up to 32 logsumexps in the lanes at once
-  float mx = -INFINITY, held = lane < n ? lse_of(lane) : -INFINITY;
-  mx = held;
+  // up to 32 logsumexps in the lanes at once, and the warp's first pieces of O on their way with them
+  const float held = lane < n ? lse_of(lane) : -INFINITY;
+  auto src_of = [&](int k) {
+    return (k < p0.n ? p0.o + p0.at(k) * D : p1.o + p1.at(k - p0.n) * D) + lane * PER;
+  };
+  constexpr int kEarly = 4;
+  float early[kEarly][PER];
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) early[i][e] = 0.f;
+    if (me + i * group < n) kv_axpy<D>(early[i], 1.f, src_of(me + i * group));
+  }
+  float mx = held;
   for (int k = 32 + lane; k < n; k += 32) mx = fmaxf(mx, lse_of(k));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float acc[PER] = {}, sum = 0.f;
-#pragma unroll 4
-  for (int k = me; k < n; k += group) {
-    const float ls = k < 32 ? __shfl_sync(0xffffffffu, held, k) : lse_of(k);
-    const float* src = k < p0.n ? p0.o + p0.at(k) * D : p1.o + p1.at(k - p0.n) * D;
-    const float wt = kv_weight(ls, mx);
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i) {
+    const int k = me + i * group;
+    if (k >= n) break;
+    const float wt = kv_weight(k < 32 ? __shfl_sync(0xffffffffu, held, k) : lse_of(k), mx);
     sum += wt;
-    kv_axpy<D>(acc, wt, src + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] += wt * early[i][e];
+  }
+#pragma unroll 4
+  for (int k = me + kEarly * group; k < n; k += group) {
+    const float wt = kv_weight(k < 32 ? __shfl_sync(0xffffffffu, held, k) : lse_of(k), mx);
+    sum += wt;
+    kv_axpy<D>(acc, wt, src_of(k));
   }
   if (group > 1) {
 #pragma unroll
@@ -770,12 +819,12 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
   pdl_wait();
   const KvCut k = a.cuts[blockIdx.x];
   if (k.n == 0) return;
-  const KvSeq s = kv_seq(a, k.b, false);
+  const KvSeq s{k.row0, k.lq, 0};
   const int group = k.n > NW ? NW : 1;
   const int rows = group == 1 ? NW : 1;  // rows a block merges at a time
   for (int r0 = blockIdx.y * rows; r0 < a.M; r0 += gridDim.y * rows) {
     const int r = r0 + (group == 1 ? warp : 0);
-    const KvRow x = kv_row_of(a, s, k.h, k.rt, r);
+    const KvRow x = kv_token_of(a, s, k.h, k.rt, r);
     if (r >= a.M || x.token < 0) continue;
     KvPieces p = kv_pieces(a, k, r), none = p;
     none.n = 0;

@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     const bool whole = part.n == n_item;
     const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * M;
     if (part.start == 0 && threadIdx.x == 0)
-      kv_record(a, line, at, blockIdx.x, line.cut(blockIdx.x) + (total - left) - at.from, n_item, whole, left == total);
+      kv_record(a, line, s, at, blockIdx.x, line.cut(blockIdx.x) + (total - left) - at.from, n_item, whole, left == total);
     if (lane == 0) s_v[warp] = vscale * kv_code_scale<FMT>();
     float* mine = reinterpret_cast<float*>(smem + L::kOffMerge) + warp * 16 * L::kRowPad;
 #pragma unroll

@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
             tc_fence_after();
             const bool whole = n == n_item;
             if (part.start == 0 && threadIdx.x == 0)
-              kv_record(a, *s_line, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left) - at.from, n_item, whole,
+              kv_record(a, *s_line, s, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left) - at.from, n_item, whole,
                         left == total);
             const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + t * 128 + r;
             float f = l == 0.f ? 0.f : vpower * (kv_code_scale<FMT>() / kv_v_shift<FMT>()) / l;

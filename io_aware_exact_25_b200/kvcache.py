@@ -42,36 +42,27 @@ class KVCache:
         if num_pages < 1 or num_kv_heads < 1:
             raise ValueError("num_pages and num_kv_heads are at least 1")
         shape = (num_pages, num_kv_heads, page_size)
-        self._adopt(torch.zeros((*shape, head_dim), dtype=torch.int8, device=device).view(dtype),
-                    torch.zeros((*shape, head_dim), dtype=torch.int8, device=device).view(dtype),
-                    torch.zeros(shape, dtype=torch.float32, device=device),
-                    torch.zeros(shape, dtype=torch.float32, device=device))
+        k, v = (torch.zeros((*shape, head_dim), dtype=torch.int8, device=device).view(dtype) for _ in range(2))
+        ks, vs = (torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2))
+        self.buffers = binding.KvBuffers(k, v, ks, vs)
 
     @classmethod
     def from_tensors(cls, k, v, k_scale, v_scale) -> "KVCache":
         """A cache over existing buffers (one layer of a larger allocation, say), which it shares."""
         self = cls.__new__(cls)
-        self._adopt(k, v, k_scale, v_scale)
+        self.buffers = binding.KvBuffers(k, v, k_scale, v_scale)
         return self
 
-    def _adopt(self, k, v, k_scale, v_scale):
-        self._abi = binding.kv_cache(k, v, k_scale, v_scale)
-        if k.shape[2] not in (16, 32, 64, 128):
-            raise ValueError("page_size is 16, 32, 64 or 128")
-        if k.shape[3] not in (64, 128):
-            raise ValueError("head_dim is 64 or 128")
-        self._tensors = (k, v, k_scale, v_scale)
-
-    k = property(lambda self: self._tensors[0])
-    v = property(lambda self: self._tensors[1])
-    k_scale = property(lambda self: self._tensors[2])
-    v_scale = property(lambda self: self._tensors[3])
-    num_pages = property(lambda self: self._tensors[0].shape[0])
-    num_kv_heads = property(lambda self: self._tensors[0].shape[1])
-    page_size = property(lambda self: self._tensors[0].shape[2])
-    head_dim = property(lambda self: self._tensors[0].shape[3])
-    dtype = property(lambda self: self._tensors[0].dtype)
-    device = property(lambda self: self._tensors[0].device)
+    k = property(lambda self: self.buffers.tensors[0])
+    v = property(lambda self: self.buffers.tensors[1])
+    k_scale = property(lambda self: self.buffers.tensors[2])
+    v_scale = property(lambda self: self.buffers.tensors[3])
+    num_pages = property(lambda self: self.buffers.num_pages)
+    num_kv_heads = property(lambda self: self.buffers.num_kv_heads)
+    page_size = property(lambda self: self.buffers.page_size)
+    head_dim = property(lambda self: self.buffers.d)
+    dtype = property(lambda self: self.k.dtype)
+    device = property(lambda self: self.buffers.device)
 
     def append(self, k, v, block_table, starts=None, cu_seqlens=None, stream=None) -> None:
         """Quantise new keys and values into the cache.
@@ -81,14 +72,12 @@ class KVCache:
         starts[b], starts[b] + 1, ... (int32 [B]; None: from 0).  Sequences may share pages, but not the slots written
         here.
         """
-        binding.kv_append(self._abi, self._tensors, k, v, block_table, starts=starts, cu_seqlens=cu_seqlens,
-                          stream=stream)
+        binding.kv_append(self.buffers, k, v, block_table, starts, cu_seqlens, stream)
 
     def read(self, block_table, cu_seqlens, total_tokens: int, starts=None, stream=None):
         """The cached keys and values as bf16 [total_tokens, num_kv_heads, head_dim]: row cu_seqlens[b] + i holds
         position starts[b] + i of sequence b (None: from 0).  Rows at or past cu_seqlens[B] are not written."""
-        return binding.kv_read(self._abi, self._tensors, block_table, total_tokens, starts=starts,
-                               cu_seqlens=cu_seqlens, stream=stream)
+        return binding.kv_read(self.buffers, block_table, total_tokens, starts, cu_seqlens, stream=stream)
 
 
 def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_q=None, max_seqlen_q: int | None = None,
@@ -127,7 +116,7 @@ def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_
         if cu_seqlens_q is not None:
             raise ValueError("cu_seqlens_q needs max_seqlen_q")
         max_seqlen_q = 1
-    o, lse = binding.fwd_kvcache(q, cache._abi, cache._tensors, block_table, seqlens, int(max_seqlen_q),
+    o, lse = binding.fwd_kvcache(q, cache.buffers, block_table, seqlens, int(max_seqlen_q),
                                  cu_seqlens_q=cu_seqlens_q, causal=causal, scale=scale, prefix_len=int(prefix_len),
                                  want_lse=return_lse, workspace=workspace, stream=stream)
     if dim == 4:

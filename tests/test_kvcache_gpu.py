@@ -262,7 +262,7 @@ def test_append_and_read_strided_views_and_rows_of_no_sequence():
     cache.append(k, v, table, cu_seqlens=cu)
     assert int((~cache.k_scale.isnan()).sum()) == 15 * Hkv
     out = torch.full((T, 2 * Hkv, d), 7.0, device="cuda").to(torch.bfloat16)
-    binding.kv_read(cache._abi, cache._tensors, table, T, cu_seqlens=cu, k=out[:, :Hkv], v=out[:, Hkv:])
+    binding.kv_read(cache.buffers, table, T, cu_seqlens=cu, k=out[:, :Hkv], v=out[:, Hkv:])
     assert (out[:2] == 7).all() and (out[17:] == 7).all()
     for x, y in ((k, out[:, :Hkv]), (v, out[:, Hkv:])):
         code, sc = quantise(x[2:17], INT8)
@@ -418,7 +418,7 @@ def test_uniform_batch_forms_views_and_untouched_rows():
     table[:, 3:3 + x.table.shape[1]] = x.table_dev
     cu = torch.tensor([2, 5, 8], dtype=torch.int32).cuda()
     l2 = torch.full((8, 10), 3.0, device="cuda")
-    binding.fwd_kvcache(wide[:, 2:10], x.cache._abi, x.cache._tensors, table[:, 3:], x.seqlens, 3, cu_seqlens_q=cu,
+    binding.fwd_kvcache(wide[:, 2:10], x.cache.buffers, table[:, 3:], x.seqlens, 3, cu_seqlens_q=cu,
                         o=out[:, :8], lse=l2)
     assert torch.equal(out[2:8, :8], o) and torch.equal(l2[:, 2:8], lse)
     assert (out[:2] == 5).all() and (out[8:] == 5).all() and (out[:, 8] == 5).all()
@@ -465,7 +465,7 @@ def test_shared_prefix_of_one_sequence_and_untouched_rows():
     l2 = torch.full((8, 6), 3.0, device="cuda")
     q = torch.zeros((6, 8, 64), device="cuda").to(torch.bfloat16)
     q[1:4] = x.q
-    binding.fwd_kvcache(q, x.cache._abi, x.cache._tensors, x.table_dev, x.seqlens, 2, cu_seqlens_q=x.cu + 1, o=out,
+    binding.fwd_kvcache(q, x.cache.buffers, x.table_dev, x.seqlens, 2, cu_seqlens_q=x.cu + 1, o=out,
                         lse=l2, prefix_len=64)
     x.check(out[1:4], l2[:, 1:4])  # (not to the bit: 24 rows may take another kernel than 12)
     assert (out[0] == 5).all() and (out[4:] == 5).all() and (l2[:, 0] == 3).all() and (l2[:, 4:] == 3).all()
