@@ -576,6 +576,7 @@ class KvBuffers:
         self.abi = FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, ps, H, d,
                              KV_FORMATS[k.dtype])
         self.ref = ctypes.byref(self.abi)
+        self.f32, self.u8 = k_scale, k.view(torch.uint8)  # whose new_empty is the quickest allocation of their types
 
 
 def _other_stream(c, stream):
@@ -715,18 +716,18 @@ def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None,
     if not _rows_usable(q):
         q = q.contiguous()
     if o is None:
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=c.device)
+        o = q.new_empty((T, Hq, d))
     else:
         _check_tokens("o", o, (T, Hq, d), c)
     if lse is not None:
         if lse.dtype != torch.float32 or lse.shape != (Hq, T) or lse.device != c.device or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on the cache's device")
     elif want_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=c.device)
+        lse = c.f32.new_empty((Hq, T))
     lib = load()
     if workspace is None:
         need = lib.fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, T, max_q, prefix_len)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=c.device)
+        workspace = c.u8.new_empty(max(need, 16))
     else:
         if workspace.device != c.device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")

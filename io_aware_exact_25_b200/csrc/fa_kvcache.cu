@@ -148,14 +148,15 @@ using Narrow = fa::KvNarrowLayout<D, D == 128 ? 2 : 3, D == 128 ? 2 : 3>;
 struct Choice {
   int M, G;
   int item_cost;  // starting and ending an item, in units of 128 keys
+  bool one_tile;  // wide kernel: at most 128 rows an item
 };
 
 Choice choose(long long rows, int d) {
   // Up to 16 rows one mma.sync tile holds an item and the cache's bytes are what is waited for.  Above, the wide
   // kernel: a 32-row narrow one spilled and was slower or no faster (24 heads over one key head, 8 sequences of 512
   // to 8192 keys: 44 us against 32; 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 254 against 266).
-  if (rows <= 16) return {16, kSms * (d == 128 ? Narrow<128>::kCtasPerSm : Narrow<64>::kCtasPerSm), 2};
-  return {256, kSms, 3};
+  if (rows <= 16) return {16, kSms * (d == 128 ? Narrow<128>::kCtasPerSm : Narrow<64>::kCtasPerSm), 2, true};
+  return {256, kSms, 3, rows <= 128};
 }
 
 // Byte offsets in the workspace: the pieces of one launch and the entries that say where they are.
@@ -179,6 +180,8 @@ size_t tiles_of(long long rows, const Choice& c) { return (size_t)((rows + c.M -
 struct Layout {
   Choice whole, prefix, suffix;
   Pieces pw, pp, ps;
+  long long items;
+  bool by_item;
   size_t prefix_o, prefix_lse, suffix_o, suffix_lse, bytes;
 };
 
@@ -188,7 +191,10 @@ Layout layout_of(int B, int Hq, int Hkv, int d, int total_q, int max_q, int pref
   const int g = Hq / Hkv;
   if (prefix_len == 0) {
     l.whole = choose((long long)max_q * g, d);
-    l.pw = place_pieces(0, l.whole, d, l.whole.G);
+    // entries by item while there are fewer items than CTAs, so that the merge has few blocks
+    l.items = (long long)B * Hkv * tiles_of((long long)max_q * g, l.whole);
+    l.by_item = l.items <= l.whole.G;
+    l.pw = place_pieces(0, l.whole, d, l.by_item ? l.items : l.whole.G);
     l.bytes = l.pw.end;
     return l;
   }
@@ -252,10 +258,10 @@ int launch_narrow(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, c
   return launch(kern, dim3(ch.G), 128, L::kSmem, st, a.phase == fa::kKvSuffix, mk, mv, a);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int CW>
 int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
-  using L = fa::KvWideLayout<D>;
-  constexpr auto kern = fa::kv_wide_kernel<D, FMT>;
+  using L = fa::KvWideLayout<D, CW>;
+  constexpr auto kern = fa::kv_wide_kernel<D, FMT, CW>;
   const int rc = allow_smem<kern>(L::kSmem);
   if (rc != FA_OK) return rc;
   return launch(kern, dim3(ch.G), L::kThreads, L::kSmem, st, a.phase == fa::kKvSuffix, a);
@@ -264,7 +270,7 @@ int launch_wide(const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
 template <int D, int FMT>
 int launch_phase_as(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
   if (ch.M == 16) return launch_narrow<D, FMT>(c, a, ch, st);
-  return launch_wide<D, FMT>(a, ch, st);
+  return ch.one_tile ? launch_wide<D, FMT, 8>(a, ch, st) : launch_wide<D, FMT, 4>(a, ch, st);
 }
 
 int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cudaStream_t st) {
@@ -275,10 +281,10 @@ int launch_phase(const fa_kv_cache* c, const fa::KvArgs& a, const Choice& ch, cu
                                  : launch_phase_as<64, fa::kKvFp8>(c, a, ch, st);
 }
 
-int launch_merge_cut(const fa::KvArgs& a, int d, const Choice& ch, cudaStream_t st) {
-  // Few items: a block for each row of a cut item, which may be in many pieces.  Many items: a block per eight rows.
-  const long long items = (long long)a.B * a.Hkv * tiles_of((long long)a.max_q * a.g, ch);
-  const dim3 grid((unsigned)ch.G, (unsigned)(items <= 64 && ch.M < 64 ? ch.M : ch.M / 8));
+int launch_merge_cut(const fa::KvArgs& a, int d, const Layout& l, cudaStream_t st) {
+  // few items: a block for each row of one, which may be in many pieces; many: a block per eight rows
+  const int M = l.whole.M;
+  const dim3 grid((unsigned)(l.by_item ? l.items : l.whole.G), (unsigned)(l.items <= 64 && M < 64 ? M : M / 8));
   return d == 64 ? launch(fa::kv_merge_cut_kernel<64>, grid, fa::kKvMergeThreads, 0, st, true, a)
                  : launch(fa::kv_merge_cut_kernel<128>, grid, fa::kKvMergeThreads, 0, st, true, a);
 }
@@ -388,6 +394,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (prefix_len == 0) {
     a.phase = fa::kKvWhole;
+    a.by_item = l.by_item;
     a.M = l.whole.M;
     a.G = l.whole.G;
     a.item_cost = l.whole.item_cost;
@@ -395,10 +402,11 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
     a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
     a.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pw.cuts);
     if ((rc = launch_phase(cache, a, l.whole, st)) != FA_OK) return rc;
-    return launch_merge_cut(a, d, l.whole, st);
+    return launch_merge_cut(a, d, l, st);
   }
   fa::KvArgs pf = a, sf = a;
   pf.phase = fa::kKvPrefix;
+  pf.by_item = 1;
   pf.M = l.prefix.M;
   pf.G = l.prefix.G;
   pf.item_cost = l.prefix.item_cost;
@@ -408,6 +416,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   pf.row_o = reinterpret_cast<float*>(ws + l.prefix_o);
   pf.row_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
   sf.phase = fa::kKvSuffix;
+  sf.by_item = 1;
   sf.M = l.suffix.M;
   sf.G = l.suffix.G;
   sf.item_cost = l.suffix.item_cost;

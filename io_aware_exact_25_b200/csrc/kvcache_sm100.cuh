@@ -56,12 +56,13 @@ struct KvArgs {
   // whole results of a phase, merged afterwards (phases other than kKvWhole)
   float* row_o;      // [total * Hq][D], normalised
   float* row_lse;    // [total * Hq], base 2
-  struct KvCut* cuts;  // where the pieces are: one entry per CTA (kKvWhole) or per item (else)
+  struct KvCut* cuts;  // where the pieces are
+  int by_item;
 };
 
-// An item's pieces: `first`, then every second one from `next` on, n in all.  kKvWhole: the entry of CTA c is the
-// item that c starts and does not finish (n = 0: none).  Other phases: the entry of an item; n = 1 is a finished item,
-// whose rows are in row_o and row_lse.
+// An item's pieces: `first`, then every second one from `next` on, n in all; n = 1 is a finished item.  The entries go
+// by item, or (by_item = 0, kKvWhole only) by CTA, CTA c's being the item that c starts and does not finish (n = 0:
+// none).  In the phases other than kKvWhole a finished item's rows are in row_o and row_lse.
 struct KvCut {
   int n, first, next, h, rt;
   int row0, lq;  // the sequence's rows
@@ -82,6 +83,26 @@ __device__ __forceinline__ int kv_find_seq(const int* cu, int B, int t, int lane
     const int skip = hits > 0 ? (hits - 1) * step : 0;
     lo += skip;
     n = min(step, n - skip);
+  }
+  return lo;
+}
+
+// The same for a token of each lane (all lanes call it): 32 samples of cu go round by shuffles, what is left is searched
+// in memory.
+__device__ __forceinline__ int kv_find_seq_lanes(const int* cu, int B, int t, int lane) {
+  const int step = (B + 31) >> 5;  // >= 1; sample i is cu[i * step]
+  const int mine = lane * step < B ? __ldg(cu + lane * step) : 0x7fffffff;
+  int i = 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const int v = __shfl_sync(0xffffffffu, mine, (i + s) & 31);
+    if (i + s < 32 && v <= t) i += s;
+  }
+  int lo = i * step, hi = min(lo + step, B);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid;
+    else hi = mid;
   }
   return lo;
 }
@@ -580,7 +601,7 @@ __device__ __forceinline__ bool kv_next(const KvArgs& a, KvSeq& s, KvPlace& p) {
   return false;
 }
 
-// Entry of an item in the phases other than kKvWhole.
+// Entry of an item.
 __device__ __forceinline__ long long kv_item_index(const KvArgs& a, int b, int h, int rt) {
   const uint32_t rows = (uint32_t)(a.phase == kKvPrefix ? a.total : a.max_q) * (uint32_t)a.g;
   const uint32_t tiles = (rows + (uint32_t)a.M - 1u) / (uint32_t)a.M;  // of the longest sequence
@@ -591,7 +612,7 @@ __device__ __forceinline__ long long kv_item_index(const KvArgs& a, int b, int h
 // first unit (as the first item of its stretch, or a later one).
 __device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, const KvSeq& s, const KvPlace& p, int c,
                                           long long w0, int n_item, bool whole, bool first_item) {
-  if (whole && a.phase == kKvWhole) return;
+  if (whole && !a.by_item) return;
   KvCut k;
   k.n = whole ? 1 : line.cta_of(w0 + a.item_cost + n_item - 1) - c + 1;
   k.first = 2 * c + (first_item ? 0 : 1);
@@ -599,7 +620,26 @@ __device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, c
   k.h = p.h, k.rt = p.rt;
   k.row0 = s.row0, k.lq = s.lq;
   k.pad = 0;
-  a.cuts[a.phase == kKvWhole ? c : kv_item_index(a, p.b, p.h, p.rt)] = k;
+  a.cuts[a.by_item ? kv_item_index(a, p.b, p.h, p.rt) : c] = k;
+}
+
+// Entries that no item will write, before anything else: a CTA's own, or those of tiles that a sequence shorter than
+// the longest does not have.
+template <bool ONE>
+__device__ __forceinline__ void kv_clear_cuts(const KvArgs& a) {
+  if (a.phase != kKvWhole) return;  // there every entry that is read has its item
+  if (!a.by_item) {
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;
+    return;
+  }
+  if (blockIdx.x != 0) return;
+  const int tiles = (int)kv_item_index(a, 0, 1, 0);  // of the longest sequence
+#pragma unroll 1
+  for (int i = threadIdx.x; i < a.B * a.Hkv; i += blockDim.x) {
+    const int b = i / a.Hkv;
+    for (int rt = kv_tiles<ONE>(a, kv_seq(a, b, false)); rt < tiles; ++rt)
+      a.cuts[kv_item_index(a, b, i - b * a.Hkv, rt)].n = 0;
+  }
 }
 
 // Where a row of an item lives: token, query head, and how many keys it sees.
@@ -614,35 +654,31 @@ __device__ __forceinline__ KvRow kv_token_of(const KvArgs& a, const KvSeq& s, in
   return KvRow{s.row0 + i, h * a.g + (int)(rr - (uint32_t)i * (uint32_t)a.g), 0};
 }
 
+// A row with its reach; every lane of the warp calls it.
 __device__ __forceinline__ KvRow kv_row_of(const KvArgs& a, const KvSeq& s, int h, int rt, int r) {
   KvRow x = kv_token_of(a, s, h, rt, r);
-  if (x.token < 0) return x;
   const int i = x.token - s.row0;
-  x.end = kv_end(a, s, i);
-  if (a.phase == kKvPrefix) {
-    // the token's own sequence bounds what it sees of the prefix
-    int b = 0, first = 0, lq = a.max_q;
-    if (a.cu) {
-      int lo = 0, hi = a.B;  // last b with cu[b] <= token
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) <= x.token) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-      const SeqSpan sp = varlen_span(a.cu, nullptr, b, a.total, a.max_q, nullptr, false);
-      first = sp.row0;
-      lq = sp.len;
-    } else {
-      b = i / a.max_q;
-      first = b * a.max_q;
-    }
-    const int at = x.token - first;
-    if (at < 0 || at >= lq) return KvRow{-1, 0, 0};  // a row of no sequence
-    const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffffffll - kKvUnit);
-    const int L = (int)min((long long)max(__ldg(a.lens + b), 0), cap);
-    x.end = min(s.lk, a.causal ? max(L - lq + at + 1, 0) : L);
+  if (a.phase != kKvPrefix) {
+    if (x.token >= 0) x.end = kv_end(a, s, i);
+    return x;
   }
+  // the token's own sequence bounds what it sees of the prefix
+  int b, first, lq;
+  if (a.cu) {
+    b = kv_find_seq_lanes(a.cu, a.B, max(x.token, 0), threadIdx.x & 31);
+    const SeqSpan sp = varlen_span(a.cu, nullptr, b, a.total, a.max_q, nullptr, false);
+    first = sp.row0;
+    lq = sp.len;
+  } else {
+    b = max(x.token, 0) / a.max_q;
+    first = b * a.max_q;
+    lq = a.max_q;
+  }
+  const int at = x.token - first;
+  if (x.token < 0 || at < 0 || at >= lq) return KvRow{-1, 0, 0};  // a row of no sequence
+  const long long cap = min((long long)a.max_pages << a.page_shift, 0x7fffffffll - kKvUnit);
+  const int L = (int)min((long long)max(__ldg(a.lens + b), 0), cap);
+  x.end = min(s.lk, a.causal ? max(L - lq + at + 1, 0) : L);
   return x;
 }
 
@@ -807,8 +843,8 @@ __device__ void kv_merge_row(const KvArgs& a, const KvRow& x, const KvPieces& p0
   if (group > 1) __syncthreads();
 }
 
-// Items that the stretches cut.  The blocks (c, .) merge the item that CTA c
-// started and left unfinished: a warp a row, or with more than eight pieces
+// Items that the stretches cut.  The blocks (i, .) merge the item of entry i,
+// if it is in pieces: a warp a row, or with more than eight pieces
 // the block a row with the pieces spread over its warps (one key head's 64K
 // keys leave over a hundred pieces, a chain that one warp would walk alone).
 template <int D>
@@ -818,7 +854,7 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
   const int warp = threadIdx.x >> 5;
   pdl_wait();
   const KvCut k = a.cuts[blockIdx.x];
-  if (k.n == 0) return;
+  if (k.n < 2 || !kv_cut_ok(a, k)) return;
   const KvSeq s{k.row0, k.lq, 0};
   const int group = k.n > NW ? NW : 1;
   const int rows = group == 1 ? NW : 1;  // rows a block merges at a time

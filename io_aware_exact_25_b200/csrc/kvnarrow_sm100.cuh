@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
   const KvLine line = kv_place<true, 128>(a, blockIdx.x, gridDim.x, reinterpret_cast<KvScan*>(smem + L::kOffScan), &b,
                                           &s, &rem);
   __syncthreads();
-  if (a.phase == kKvWhole && threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;  // until this CTA leaves an item unfinished
+  kv_clear_cuts<true>(a);
   if (b < 0 || *abort_flag) {
     if (a.phase == kKvSuffix) pdl_wait();
     return;

@@ -8,11 +8,16 @@
 // from.  Warp roles:
 //   warps 0-3   softmax of tile 0 (a thread per row; they also load Q)
 //   warps 4-7   softmax of tile 1
-//   warps 8-11  converter: codes to f16 operand tiles
-//   warp  12    MMA issue (one thread)
-//   warp  13    producer: codes and scales from the cache's pages to shared
+//   then CW     converter: codes to f16 operand tiles
+//   then one    MMA issue (one thread)
+//   then one    producer: codes and scales from the cache's pages to shared
 //               memory by bulk copies, a page (or 128 rows) at a time;
-//               warps 14-15 complete the warpgroup
+//               and two that complete the warpgroup
+// CW is 4, or 8 where items have at most 128 rows (one tile, whose softmax is
+// faster than 4 converter warps, about 4900 clocks a key tile: 64 sequences of
+// drafts of 1 to 5 tokens, 6 heads a group, 256 us with 4, 212 with 8; with two
+// tiles the 8 take issue slots from the softmax: a prompt's chunk, 16 heads, 245
+// us with 4, 271 with 8).
 // The converter threads take 16 codes at a time, unpack them exactly as the
 // narrow kernel does and write the f16 tile in the 128-byte swizzled layout the
 // MMA reads: 256 rows share one conversion.  (They first loaded the codes
@@ -43,15 +48,19 @@
 
 namespace fa {
 
-template <int D>
+template <int D, int CW>
 struct KvWideLayout {
   static constexpr int kM = 256;
-  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+  static constexpr int kSoftmaxWarps = 8, kConvertWarps = CW;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);
   static constexpr int kConvert = 32 * kConvertWarps;
-  // launched at 128 registers a thread: 256 x 192 + 128 x 72 + 128 x 56 = 512 x 128
-  static constexpr uint32_t kRegsSoftmax = 192, kRegsConvert = 72, kRegsCtl = 56;
-  static_assert(256 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsCtl <= 128 * kThreads, "register split");
+  // launched at 128 registers a thread with 4 converter warps (512 x 128 = 256 x 192 + 128 x 72 + 128 x 56), at 96
+  // with 8 (640 x 96 = 256 x 176 + 256 x 48 + 128 x 32)
+  static constexpr uint32_t kRegsLaunch = CW == 4 ? 128 : 96;
+  static constexpr uint32_t kRegsSoftmax = CW == 4 ? 192 : 176, kRegsConvert = CW == 4 ? 72 : 48;
+  static constexpr uint32_t kRegsCtl = CW == 4 ? 56 : 32;
+  static_assert(CW == 4 || CW == 8, "whole warpgroups");
+  static_assert(256 * kRegsSoftmax + 32 * CW * kRegsConvert + 128 * kRegsCtl <= kRegsLaunch * kThreads, "register split");
   static constexpr uint32_t kHalf = 128u * 128u;    // 128 rows x 64 f16 columns
   static constexpr uint32_t kTile = 128u * D * 2u;  // 128 x D f16
   // K/V operand ring.  Four tiles: K(j + 1) then takes the place of K(j - 1), which the step before freed; with three
@@ -137,24 +146,24 @@ __device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(const KvArgs a) {
-  using L = KvWideLayout<D>;
+template <int D, int FMT, int CW>
+__global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kernel(const KvArgs a) {
+  using L = KvWideLayout<D, CW>;
   extern __shared__ __align__(1024) uint8_t smem[];
   // (through a shuffle: the roles' branches are then uniform to the compiler)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* bar_q = bars;                              // [2] Q_t written (128 arrivals)
-  uint64_t* bar_kv_full = bars + 2;                    // [S] operand tile written (128)
+  uint64_t* bar_kv_full = bars + 2;                    // [S] operand tile written
   uint64_t* bar_kv_empty = bar_kv_full + L::kStages;   // [S] operand tile consumed
   uint64_t* bar_raw_full = bar_kv_empty + L::kStages;  // [R] codes landed
-  uint64_t* bar_raw_empty = bar_raw_full + L::kRaw;    // [R] codes converted (4 warps)
+  uint64_t* bar_raw_empty = bar_raw_full + L::kRaw;    // [R] codes converted
   uint64_t* bar_s = bar_raw_empty + L::kRaw;           // [2] S_t ready
   uint64_t* bar_p = bar_s + 2;                         // [2][2] half h of P_t written (128)
   uint64_t* bar_pv = bar_p + 4;                        // [2] O_t += P_t V done
   uint64_t* bar_sc_full = bar_pv + 2;                  // [2] scales of a key tile written (128)
   uint64_t* bar_sc_empty = bar_sc_full + 2;            // [2] scales consumed (8 warps)
-  uint64_t* bar_vmax = bar_sc_empty + 2;               //     the converter warps' V maxima written (4)
+  uint64_t* bar_vmax = bar_sc_empty + 2;               //     the converter warps' V maxima written
   uint64_t* bar_drain = bar_vmax + 1;                  //     every MMA retired
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -202,7 +211,7 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Abort ab{abort_flag, a.err};
   const bool run = b >= 0 && *abort_flag == 0;
-  if (a.phase == kKvWhole && threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;  // until this CTA leaves an item unfinished
+  kv_clear_cuts<false>(a);
   const int total = b >= 0 ? (int)(line.cut(blockIdx.x + 1) - line.cut(blockIdx.x)) : 0;  // this CTA's units
   KvLine* s_line = reinterpret_cast<KvLine*>(smem + L::kOffScan);  // kept for kv_record only (the scan is over)
   if (threadIdx.x == 0) *s_line = line;
@@ -362,12 +371,13 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
       const int tid = threadIdx.x - 32 * L::kSoftmaxWarps;
       const int cw = warp - L::kSoftmaxWarps;
       const int ch = tid % CH, r_in = tid / CH;
-      // the chunk's place in row r of the operand tile: 16 f16 columns are two 16-byte chunks of the 64-column half
+      // the chunk's place in its row of the operand tile: 16 f16 columns are two 16-byte chunks of the 64-column half
       // ch / 4.  At d = 128 eight lanes store one row, and those of the upper half write the second one first, so that
       // the eight cover all banks; at d = 64 they store two rows, whose swizzles differ already.
-      const uint32_t half_off = (uint32_t)(ch >> 2) * L::kHalf;
-      const int c0 = 2 * (ch & 3);
-      const int swap = D == 128 ? (ch >> 2) & 1 : 0;
+      const int c0 = 2 * (ch & 3), swap = D == 128 ? (ch >> 2) & 1 : 0;
+      static_assert(RP % 8 == 0, "a thread's rows share their swizzle");
+      const uint32_t row_off = (uint32_t)(ch >> 2) * L::kHalf + r_in * 128;
+      const uint32_t off0 = row_off + (((c0 + swap) ^ (r_in & 7)) << 4), off1 = row_off + (((c0 + 1 - swap) ^ (r_in & 7)) << 4);
       uint32_t pos = 0, nsc = 0;
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
@@ -386,10 +396,9 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
 #pragma unroll
           for (int i = 0; i < NP; ++i) raw[i] = ld_shared_u4(src + (i * RP + r_in) * D);
           if (!mbar_wait_warp(&bar_kv_empty[st], ((pos / L::kStages) & 1u) ^ 1u, ab)) return false;
-          const uint32_t tile = sbase + L::kOffKV + st * L::kTile + half_off;
+          const uint32_t tile = sbase + L::kOffKV + st * L::kTile;
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const int r = i * RP + r_in;
             uint32_t w[8];
             kv_unpack<FMT>(raw[i].x, w[0], w[1]);
             kv_unpack<FMT>(raw[i].y, w[2], w[3]);
@@ -403,14 +412,13 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
                 w[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
             }
-            const uint32_t row = tile + r * 128;
-            const uint32_t a0 = row + ((c0 ^ (r & 7)) << 4), a1 = row + (((c0 + 1) ^ (r & 7)) << 4);
+            const uint32_t at0 = tile + off0 + i * (RP * 128), at1 = tile + off1 + i * (RP * 128);
             if (swap) {
-              st_shared_v4(a1, w[4], w[5], w[6], w[7]);
-              st_shared_v4(a0, w[0], w[1], w[2], w[3]);
+              st_shared_v4(at0, w[4], w[5], w[6], w[7]);
+              st_shared_v4(at1, w[0], w[1], w[2], w[3]);
             } else {
-              st_shared_v4(a0, w[0], w[1], w[2], w[3]);
-              st_shared_v4(a1, w[4], w[5], w[6], w[7]);
+              st_shared_v4(at0, w[0], w[1], w[2], w[3]);
+              st_shared_v4(at1, w[4], w[5], w[6], w[7]);
             }
           }
           fence_proxy_async_smem();
@@ -426,21 +434,22 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
           if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
           const uint32_t raw_sc = sbase + L::kOffRawScale + (sl >> 1) * 1024;
           const int key0 = first + j * kKvUnit;
-          const bool in = key0 + tid < item_end;
-          const float ks = in ? ld_shared_f(raw_sc + 4 * tid) : 0.f;
-          const float vk = in ? ld_shared_f(raw_sc + 512 + 4 * tid) : 0.f;
+          const int key = tid & 127;  // whose scales warps 0-3 publish
+          const bool in = key0 + key < item_end;
+          const float ks = in ? ld_shared_f(raw_sc + 4 * key) : 0.f;
+          const float vk = in ? ld_shared_f(raw_sc + 512 + 4 * key) : 0.f;
           float vs[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) vs[i] = ld_shared_f(raw_sc + 512 + 4 * (i * RP + r_in));
-          // the largest V scale of the tile: each warp leaves its own, all read (a bounded wait, so that an aborting CTA
+          // the largest V scale of the tile: warps 0-3 leave theirs, all read (a bounded wait, so that an aborting CTA
           // cannot strand a warp at a barrier)
           const uint32_t red = smisc + 64 + (nsc & 1u) * 16;
           const uint32_t vb = __float_as_uint(vk) & 0x7fffffffu;
           const uint32_t vnan = __ballot_sync(0xffffffffu, vb > 0x7f800000u);
           const uint32_t wmax = __reduce_max_sync(0xffffffffu, vb >= 0x7f800000u ? 0u : vb);
           if (lane == 0) {
-            st_shared_f(red + 4 * cw, __uint_as_float(wmax));
-            mbar_arrive(bar_vmax);
+            if (cw < 4) st_shared_f(red + 4 * cw, __uint_as_float(wmax));
+            mbar_arrive(bar_vmax);  // all of them, so that none can run a tile ahead of another's wait
           }
           if (!(ok = mbar_wait_warp(bar_vmax, nsc & 1u, ab))) break;
           const float4 m4 = ld_shared_f4(red);  // all positive: as integers they sort alike
@@ -456,11 +465,13 @@ __global__ void __launch_bounds__(KvWideLayout<D>::kThreads, 1) kv_wide_kernel(c
             ratio[i] = f == f ? pack_f16x2(f, f) : 0u;
           }
           const uint32_t st = nsc & 1u;
-          if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
-          st_shared_f(sscale + st * 512 + 4 * tid, ks * (a.scale_log2 * kv_code_scale<FMT>()));
-          if (lane == 0) st_shared_f(smisc + st * 32 + 16 + 4 * cw, __uint_as_float(vnan));
-          if (tid == 0) st_shared_f(smisc + st * 32, vpower);
-          mbar_arrive(&bar_sc_full[st]);
+          if (cw < 4) {
+            if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
+            st_shared_f(sscale + st * 512 + 4 * tid, ks * (a.scale_log2 * kv_code_scale<FMT>()));
+            if (lane == 0) st_shared_f(smisc + st * 32 + 16 + 4 * cw, __uint_as_float(vnan));
+            if (tid == 0) st_shared_f(smisc + st * 32, vpower);
+            mbar_arrive(&bar_sc_full[st]);
+          }
           ++nsc;
           if (!(ok = convert(nullptr))) break;
           if (!(ok = convert(ratio))) break;
