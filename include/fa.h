@@ -351,7 +351,8 @@ int fa_bwd_recompute_range(const void* q, const void* k, const void* v, const vo
  *   FA_KV_FP8:  scale = amax / 448, code = 448 x / amax rounded to e4m3
  * with amax = max |x|, rounding half to even, and stands for code * scale.  A
  * row of zeros has scale 0; a row with an infinity or a NaN has a NaN scale, so
- * every value of it reads as NaN.  page_size is 16, 32, 64 or 128; d is 64 or
+ * every value of it reads as NaN, and attention makes NaN of the query rows that
+ * see it and of no others.  page_size is 16, 32, 64 or 128; d is 64 or
  * 128; num_pages * num_kv_heads * page_size is below 2^31.
  *
  * block_table: device int32 [B][max_pages], rows table_stride elements apart:
@@ -407,9 +408,13 @@ int fa_kv_read(const fa_kv_cache* cache, void* k, void* v, const fa_strides* str
  * [B]).  Of its L queries, query i sees keys j < seqlens[b], and when causal
  * j < seqlens[b] - L + i + 1: the queries are the sequence's last tokens.  A
  * query that sees no key gets o = 0 and lse = -inf; rows of no sequence are
- * left as they were.  The dequantised keys and values enter the products
- * exactly, the probabilities rounded to f16.  Results do not depend on the
- * workspace's contents and are the same from run to run.
+ * left as they were.  o must not overlap the inputs.  A sequence with more than
+ * max_q query rows is cut to them (device error 3).  Scores are summed in fp32
+ * from exact products of q and the codes; the probabilities are rounded to f16
+ * for their products with the values, and with more than 16 rows per key head
+ * (max_q * Hq / num_kv_heads, or that of the whole batch for the prefix) the
+ * values to f16 too.  Results do not depend on the workspace's contents and are
+ * the same from run to run.
  *
  * prefix_len > 0 (a multiple of page_size, at most max_pages * page_size)
  * declares that every sequence's first prefix_len keys are the same pages --

@@ -576,7 +576,9 @@ class KvBuffers:
         self.abi = FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, ps, H, d,
                              KV_FORMATS[k.dtype])
         self.ref = ctypes.byref(self.abi)
-        self.f32, self.u8 = k_scale, k.view(torch.uint8)  # whose new_empty is the quickest allocation of their types
+        # whose new_empty is the quickest allocation of their types
+        self.f32, self.u8 = k_scale, k.view(torch.uint8)
+        self.bf16 = torch.empty(0, dtype=torch.bfloat16, device=k.device)
 
 
 def _other_stream(c, stream):
@@ -661,11 +663,11 @@ def kv_read(c: KvBuffers, block_table, total_tokens, starts=None, cu_seqlens=Non
             return kv_read(c, block_table, total_tokens, starts, cu_seqlens, k, v)
     shape = (int(total_tokens), c.num_kv_heads, c.d)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+        k = c.bf16.new_empty(shape)
     else:
         _check_tokens("k", k, shape, c)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+        v = c.bf16.new_empty(shape)
     else:
         _check_tokens("v", v, shape, c)
     _kv_rows(load().fa_kv_read, "fa_kv_read", c, k, v, shape[0], block_table, starts, cu_seqlens)

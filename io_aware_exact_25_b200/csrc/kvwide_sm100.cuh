@@ -32,8 +32,8 @@
 // codes during the conversion, as f16 ratios to a running power of two above
 // every V scale seen (two f16 roundings, 2^-11 each; with the factor
 // kv_v_shift the products stay in f16's normal range down to 2^-22 of the
-// largest scale).  A V scale that is NaN would spoil rows that do not see its
-// key, 0 x NaN: its row enters as zeros, and the rows that see it are made NaN
+// largest scale).  A V scale that is not finite would spoil rows that do not see
+// its key, 0 x NaN: its row enters as zeros, and the rows that see it are made NaN
 // at the end, from a bit set of such keys per tile.  q goes into f16 as it is
 // if the row's largest entry is in [2^-1, 2^15), and shifted by a power of two
 // that its scores take back otherwise.
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           // cannot strand a warp at a barrier)
           const uint32_t red = smisc + 64 + (nsc & 1u) * 16;
           const uint32_t vb = __float_as_uint(vk) & 0x7fffffffu;
-          const uint32_t vnan = __ballot_sync(0xffffffffu, vb > 0x7f800000u);
+          const uint32_t vnan = __ballot_sync(0xffffffffu, vb >= 0x7f800000u);
           const uint32_t wmax = __reduce_max_sync(0xffffffffu, vb >= 0x7f800000u ? 0u : vb);
           if (lane == 0) {
             if (cw < 4) st_shared_f(red + 4 * cw, __uint_as_float(wmax));
@@ -461,8 +461,9 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           uint32_t ratio[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            const float f = key0 + i * RP + r_in < item_end ? vs[i] * vinv * kv_v_shift<FMT>() : 0.f;
-            ratio[i] = f == f ? pack_f16x2(f, f) : 0u;
+            const bool use = key0 + i * RP + r_in < item_end && (__float_as_uint(vs[i]) & 0x7fffffffu) < 0x7f800000u;
+            const float f = use ? vs[i] * vinv * kv_v_shift<FMT>() : 0.f;
+            ratio[i] = pack_f16x2(f, f);
           }
           const uint32_t st = nsc & 1u;
           if (cw < 4) {
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           }
           const bool shifted = __any_sync(0xffffffffu, up != 1.f);
           float m = 0.f, l = 0.f, vpower = 0.f;  // m means nothing while l = 0
-          bool spoiled = false;                  // the row sees a key whose V scale is NaN
+          bool spoiled = false;                  // the row sees a key whose V scale is not finite
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const uint32_t st = nsc & 1u;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
                 if (c >= lim) w[c >> 5][c & 31] = 0xff800000u;
             }
             {
-              // keys with a NaN V scale: does the row see one?
+              // keys whose V scale is not finite: does the row see one?
               const uint32_t nb[4] = {__float_as_uint(nan4.x), __float_as_uint(nan4.y), __float_as_uint(nan4.z),
                                       __float_as_uint(nan4.w)};
               if ((nb[0] | nb[1] | nb[2] | nb[3]) != 0u) {

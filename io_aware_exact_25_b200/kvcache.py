@@ -99,6 +99,11 @@ def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_
     ``workspace`` (a CUDA tensor of at least ``binding.fwd_kvcache_workspace_size`` bytes) is allocated if not given.
     No gradients.
     """
+    ctx = binding._other_stream(cache.buffers, stream)
+    if ctx is not None:
+        with ctx:
+            return flash_attention_kvcache(q, cache, block_table, seqlens, cu_seqlens_q, max_seqlen_q, causal, scale,
+                                           prefix_len, return_lse, workspace)
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("flash_attention_kvcache has no backward: detach q or use torch.no_grad()")
     dim = q.dim()
@@ -118,7 +123,7 @@ def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_
         max_seqlen_q = 1
     o, lse = binding.fwd_kvcache(q, cache.buffers, block_table, seqlens, int(max_seqlen_q),
                                  cu_seqlens_q=cu_seqlens_q, causal=causal, scale=scale, prefix_len=int(prefix_len),
-                                 want_lse=return_lse, workspace=workspace, stream=stream)
+                                 want_lse=return_lse, workspace=workspace)
     if dim == 4:
         o = o.view(shape)
     return (o, lse) if return_lse else o

@@ -6,8 +6,10 @@ Tolerances are derived, not fitted.  For row i of one head, with x the fp64 scor
             instead of rounding; q's f16 form is exact above 2^-14 of the row's largest entry and off by at most
             2^-24 of it below: 2^-24 Y, Y = max_j scale max_c |q_c| sum_c |k_jc|; the exponent argument and the
             exponential add 2^-21 (1 + max |x|).  Their sum is delta.
-  o         2^-8 |o| (the output's bf16 rounding) + A (2^-11 + 2 delta), A = sum_j p_j |v_j|, 2^-11 for the f16
-            rounding of p, + N 2^-32 V for probabilities below f16's normal range (each off by at most 2^-25 on a
+  o         2^-8 |o| (the output's bf16 rounding) + A (r 2^-11 + 2 delta), A = sum_j p_j |v_j|.  r counts the f16
+            roundings, of p, and above 16 rows per key head of the value's scale and of the scaled value: 1 or 3; the
+            latter two are also off by at most 2^-25 V where they leave f16's normal range, 2^-22 below the largest
+            scale.  + N 2^-32 V for probabilities below f16's normal range (each off by at most 2^-25 on a
             scale where the row sum is at least 2^7), V = max |v|, + 2^-20 A for fp32 sums and the merge.
   lse       delta + 2^-20 (1 + |lse|)
 The cache's codes have to equal those of the exact quotient bit for bit; scales are one fp32 division, so they do too.
@@ -108,6 +110,8 @@ class Batch:
 
     def check(self, o, lse, causal=True, scale=None):
         scale = scale or 1.0 / math.sqrt(self.d)
+        wide = max(self.q_lens + [self.T if self.prefix else 0]) * self.g > 16
+        r, sub = (3, 2.0 ** -25) if wide else (1, 0.0)
         t = 0
         for b, (nq, n) in enumerate(zip(self.q_lens, self.lens)):
             k, v = self.values("k", b), self.values("v", b)
@@ -133,8 +137,8 @@ class Batch:
                 big = x.abs().masked_fill(~sees, 0).amax(1)
                 delta = 4 * (self.d + 16) * 2.0 ** -24 * X + 2.0 ** -24 * Y + 2.0 ** -21 * (1 + big)
                 V = torch.stack([vv[s].abs().max() if s.any() else vv.new_zeros(()) for s in sees])
-                tol = 2.0 ** -8 * ref.abs() + A * (2.0 ** -11 + 2.0 ** -20 + 2 * delta)[:, None] \
-                    + (n * 2.0 ** -32 * V)[:, None]
+                tol = 2.0 ** -8 * ref.abs() + A * (r * 2.0 ** -11 + 2.0 ** -20 + 2 * delta)[:, None] \
+                    + ((n * 2.0 ** -32 + sub) * V)[:, None]
                 ok = ~empty
                 bad = (got - ref).abs()[ok] - tol[ok]
                 assert not torch.isnan(got[ok]).any()
@@ -380,7 +384,7 @@ def test_long_cache_past_32_bit_offsets():
     assert torch.equal(kr, (code.float() * sc[..., None]).to(torch.bfloat16).cuda())
     for nq in (1, 50):
         x = Batch.__new__(Batch)
-        x.B, x.q_lens, x.lens, x.prefix, x.Hkv, x.g, x.d, x.page = 1, [nq], [L], 0, Hkv, 2, d, page
+        x.B, x.q_lens, x.lens, x.prefix, x.Hkv, x.g, x.d, x.page, x.T = 1, [nq], [L], 0, Hkv, 2, d, page, nq
         x.cache, x.table, x.table_dev = cache, table, table.cuda()
         x.cu, x.seqlens = torch.tensor([0, nq], dtype=torch.int32).cuda(), torch.tensor([L], dtype=torch.int32).cuda()
         x.q = torch.randn((nq, 2 * Hkv, d), generator=gen).to(torch.bfloat16).cuda()
@@ -494,7 +498,7 @@ def test_a_prompt_and_its_answers(dtype, d, Hkv, g):
         start = torch.tensor([first], dtype=torch.int32).cuda()
         cache.append(k[first:first + n], v[first:first + n], x.table_dev, start, cu_seqlens=cu)
         x.q = torch.randn((n, Hkv * g, d), generator=gen).to(torch.bfloat16).cuda()
-        x.q_lens, x.lens, x.cu, x.seqlens = [n], [first + n], cu, start + n
+        x.q_lens, x.lens, x.cu, x.seqlens, x.T = [n], [first + n], cu, start + n, n
         x.check(*x.run())
     # the answers: the full pages are shared, the prompt's tail is written to each answer's own page
     table = torch.full((A, 16), -1, dtype=torch.int32)
@@ -507,7 +511,7 @@ def test_a_prompt_and_its_answers(dtype, d, Hkv, g):
     cache.append(kt, vt, x.table_dev, torch.full((A,), whole * page, dtype=torch.int32).cuda(),
                  cu_seqlens=(torch.arange(A + 1, dtype=torch.int32) * tail).cuda())
     lens = torch.full((A,), P, dtype=torch.int32).cuda()
-    x.q_lens, x.cu = [1] * A, torch.arange(A + 1, dtype=torch.int32).cuda()
+    x.q_lens, x.cu, x.T = [1] * A, torch.arange(A + 1, dtype=torch.int32).cuda(), A
     for step in range(steps):
         kn, vn = (torch.randn((A, Hkv, d), generator=gen).to(torch.bfloat16).cuda() for _ in "kv")
         cache.append(kn, vn, x.table_dev, lens)
@@ -596,6 +600,71 @@ def test_calls_on_other_streams():
     for i in range(2):
         for o, lse in outs[i]:
             assert torch.equal(o, ref[i][0]) and torch.equal(lse, ref[i][1])
+    # a layout that is copied first, on the stream the call was given
+    q = xs[0].q.view(4, 1, 8, 128).transpose(2, 3).contiguous().transpose(2, 3)
+    torch.cuda.synchronize()
+    o = flash_attention_kvcache(q, xs[0].cache, xs[0].table_dev, xs[0].seqlens, stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(o.view(4, 8, 128), ref[0][0])
+
+
+def test_empty_calls():
+    x = Batch(INT8, 64, 16, 1, 2, q=[1, 1], lens=[20, 32], seed=51)
+    c, dev = x.cache, "cuda"
+    no_rows = torch.empty((0, 1, 64), dtype=torch.bfloat16, device=dev)
+    zero = torch.zeros(3, dtype=torch.int32, device=dev)
+    before = c.k_scale.clone()
+    c.append(no_rows, no_rows, x.table_dev, cu_seqlens=zero)
+    k, v = c.read(x.table_dev, zero, 0)
+    assert k.shape == v.shape == (0, 1, 64)
+    assert torch.equal(before.nan_to_num(-1), c.k_scale.nan_to_num(-1))
+    o, lse = flash_attention_kvcache(torch.empty((0, 2, 64), dtype=torch.bfloat16, device=dev), c, x.table_dev, x.seqlens,
+                                     cu_seqlens_q=zero, max_seqlen_q=1, return_lse=True)
+    assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
+    none = torch.empty((0,), dtype=torch.int32, device=dev)
+    o = flash_attention_kvcache(torch.empty((0, 1, 2, 64), dtype=torch.bfloat16, device=dev), c,
+                                torch.empty((0, 2), dtype=torch.int32, device=dev), none)
+    assert o.shape == (0, 1, 2, 64)
+    assert binding.device_error() == 0
+
+
+def test_python_refusals():
+    x = Batch(INT8, 64, 16, 2, 2, q=[1, 1], lens=[20, 32], seed=52)
+    ok = dict(cu_seqlens_q=x.cu, max_seqlen_q=1)
+    call = lambda q=x.q, table=x.table_dev, lens=x.seqlens, **kw: flash_attention_kvcache(q, x.cache, table, lens,
+                                                                                          **{**ok, **kw})
+    call()
+    for bad in (dict(q=x.q.float()), dict(q=x.q[:, :3]), dict(q=x.q[..., :32]), dict(table=x.table_dev.long()),
+                dict(table=x.table_dev[0]), dict(table=x.table_dev[:1].expand(2, -1)), dict(lens=x.seqlens[:1]),
+                dict(lens=x.seqlens.long()), dict(cu_seqlens_q=x.cu[:2]), dict(max_seqlen_q=None),
+                dict(prefix_len=8), dict(prefix_len=1 << 20), dict(prefix_len=-16),
+                dict(q=x.q.clone().requires_grad_()), dict(table=x.table),
+                dict(q=x.q.view(1, 2, 4, 64)), dict(workspace=torch.empty(16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(binding.FaError):
+        call(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(binding.FaError):
+        call(scale=-1.0)
+    kv = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for args in ((kv.float(), kv), (kv[:, :1], kv), (kv, kv[:1]), (kv[:1], kv[:1])):
+        with pytest.raises(ValueError):
+            x.cache.append(*args, x.table_dev)
+    with pytest.raises(ValueError):
+        KVCache.from_tensors(x.cache.k, x.cache.v.view(FP8), x.cache.k_scale, x.cache.v_scale)
+    with pytest.raises(ValueError):
+        KVCache.from_tensors(x.cache.k[:, :, :15], x.cache.v[:, :, :15], x.cache.k_scale, x.cache.v_scale)
+    assert binding.device_error() == 0
+
+
+@pytest.mark.parametrize("g", [2, 20, 80])
+def test_an_infinite_scale_spoils_only_the_rows_that_see_it(g):
+    x = Batch(INT8, 128, 16, 1, g, q=[4, 2], lens=[200, 64], seed=53)
+    clean, clean_lse = x.run()
+    x.cache.v_scale[x.table[0, 198 // 16].item(), :, 198 % 16] = float("inf")
+    o, lse = x.run()
+    assert not o[2:4].isfinite().any() and torch.equal(lse, clean_lse)
+    assert torch.equal(o[:2], clean[:2]) and torch.equal(o[4:], clean[4:])
 
 
 def test_lengths_out_of_range_are_clamped_and_reported():
