@@ -105,10 +105,10 @@ int rows_setup(const fa_kv_cache* c, const void* k, const void* v, const fa_stri
 
 template <int D>
 int launch_rows(const fa::KvArgs& a, int format, bool append, cudaStream_t st) {
-  const long long units = (2ll * a.Hkv + fa::kv_rows_per_unit<D>() - 1) / fa::kv_rows_per_unit<D>() * a.total;
-  const long long blocks = (units + 7) / 8;
-  if (blocks > 0x7fffffffll) return FA_ERR_TOO_LARGE;
-  const unsigned grid = (unsigned)blocks;
+  const int rows = fa::kv_rows_per_warp<D>();
+  const long long warps = 2ll * ((a.Hkv + rows - 1) / rows) * a.total;
+  if (warps > 0x7fffffffll) return FA_ERR_TOO_LARGE;  // more rows than a cache can have
+  const unsigned grid = (unsigned)((warps + 7) / 8);
   if (append) {
     if (format == FA_KV_INT8) fa::kv_append_kernel<D, fa::kKvInt8><<<grid, 256, 0, st>>>(a);
     else fa::kv_append_kernel<D, fa::kKvFp8><<<grid, 256, 0, st>>>(a);

@@ -109,7 +109,7 @@ __device__ __forceinline__ int kv_find_seq_lanes(const int* cu, int B, int t, in
 
 // Row of the cache's [page, head, slot] grid that holds position pos of sequence b and head 0, or -1 (and a
 // device error) where the block table has no such page.  Head h is h << page_shift rows further on.
-__device__ __forceinline__ long long kv_row(const KvArgs& a, int b, long long pos, bool report) {
+__device__ __forceinline__ int kv_row(const KvArgs& a, int b, long long pos, bool report) {
   const long long pi = pos >> a.page_shift;
   int page = -1;
   if (pos >= 0 && pi < a.max_pages) page = __ldg(a.table + b * a.table_stride + pi);
@@ -117,7 +117,7 @@ __device__ __forceinline__ long long kv_row(const KvArgs& a, int b, long long po
     if (report && a.err) atomicCAS(a.err, kDevOk, kDevBadPage);
     return -1;
   }
-  return (((long long)page * a.Hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  return ((page * a.Hkv) << a.page_shift) + (int)(pos & ((1 << a.page_shift) - 1));  // rows are fewer than 2^31
 }
 
 // x / y for x >= 0, y > 0; almost always of 32-bit numbers, whose division is several times shorter.
@@ -177,36 +177,81 @@ __device__ __forceinline__ uint32_t kv_encode4(uint64_t y01, uint64_t y23) {
   }
 }
 
+// The codes of a word times scale2 = (scale, scale), as four bf16.
 template <int FMT>
-__device__ __forceinline__ void kv_decode4(uint32_t w, float (&x)[4]) {
+__device__ __forceinline__ uint2 kv_decode4(uint32_t w, uint64_t scale2) {
+  uint64_t x01, x23;
   if constexpr (FMT == kKvInt8) {
     const uint32_t u = w ^ 0x80808080u;  // code + 128 in each byte
     // 2^23 + byte as a float, minus 2^23 + 128
-    x[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f;
-    x[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f;
-    x[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.f;
-    x[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
+    const uint64_t bias = f2_pack(-8388736.f, -8388736.f);
+    x01 = f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)),
+                         __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441))), bias);
+    x23 = f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)),
+                         __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443))), bias);
   } else {
     uint32_t lo, hi;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
     const float2 p = __half22float2(*reinterpret_cast<__half2*>(&lo));
     const float2 q = __half22float2(*reinterpret_cast<__half2*>(&hi));
-    x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;
+    x01 = f2_pack(p.x, p.y);
+    x23 = f2_pack(q.x, q.y);
   }
+  // (not f2_mul, which flushes the scales of the smallest rows)
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x01) : "l"(x01), "l"(scale2));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x23) : "l"(x23), "l"(scale2));
+  float a, b, c, d;
+  f2_unpack(x01, a, b);
+  f2_unpack(x23, c, d);
+  return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
 // ----------------------------------------------------------- append, read
 
 // Append and read share their decomposition.  A cache row of d codes is the
 // work of d / 8 lanes, 16 bytes of bf16 against 8 bytes of codes each, so one
-// warp moves 32 / (d / 8) rows at a time and kKvUnroll times that in one unit,
-// all loads ahead of all stores.  The rows of a token are its Hkv key rows
-// and then its Hkv value rows.  Both directions are bound by memory.
+// warp moves 32 / (d / 8) rows at a time and kKvUnroll times that in all, every
+// load ahead of every store.  A warp's rows are heads of one token's keys or of
+// its values.  Reading back is bound by memory (append and read of 61298 tokens,
+// 16 heads, d = 128: 761 MB each way); appending is bound by instruction issue,
+// about 100 per lane and row pair.
 constexpr int kKvUnroll = 4;
 
 template <int D>
-__host__ __device__ constexpr int kv_rows_per_unit() { return 32 / (D / 8) * kKvUnroll; }
+__host__ __device__ constexpr int kv_rows_per_warp() { return 32 / (D / 8) * kKvUnroll; }
+
+// A warp's token, tensor and heads, and where its sequence keeps them.
+struct KvMove {
+  int t, h0;       // token; this lane's first head; t < 0: nothing to do
+  bool value;      // V instead of K
+};
+
+template <int D>
+__device__ __forceinline__ KvMove kv_move(const KvArgs& a, int lane) {
+  const uint32_t per = (uint32_t)(a.Hkv + kv_rows_per_warp<D>() - 1) / (uint32_t)kv_rows_per_warp<D>();
+  const uint32_t w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t tv = w / per;  // 2 token + (0: keys, 1: values)
+  KvMove m;
+  m.t = (int)(tv >> 1);
+  m.value = (tv & 1u) != 0u;
+  m.h0 = (int)(w - tv * per) * kv_rows_per_warp<D>() + lane / (D / 8);
+  if (m.t >= a.total) m.t = -1;
+  return m;
+}
+
+// The cache row of head 0 of token t, or -1: a row of no sequence, or (and a device error) one without a page.
+__device__ __forceinline__ int kv_place_token(const KvArgs& a, int t, int lane, bool* in_sequence) {
+  int b = t, first = t, end = t + 1;
+  if (a.cu) {
+    b = kv_find_seq(a.cu, a.B, t, lane);
+    first = __ldg(a.cu + b);
+    end = __ldg(a.cu + b + 1);
+  }
+  *in_sequence = t >= first && t < end;
+  if (!*in_sequence) return -1;
+  return kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
+}
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
@@ -215,31 +260,19 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
   constexpr uint32_t kTinyBits = (127u - 100u) << 7;  // 2^-100 as a bf16
   static_assert(kKvUnroll % 2 == 0, "rows go through the shuffles in pairs");
   const int lane = threadIdx.x & 31;
-  const int units = (2 * a.Hkv + kv_rows_per_unit<D>() - 1) / kv_rows_per_unit<D>();  // per token
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(w / units);
-  if (t >= a.total) return;
-  const int r0 = (int)(w - (long long)t * units) * kv_rows_per_unit<D>() + lane / LPR;
   const int col = (lane % LPR) * 8;
+  const KvMove mv = kv_move<D>(a, lane);
+  if (mv.t < 0) return;
+  const long long sh = mv.value ? a.xv_sh : a.xk_sh;
+  const __nv_bfloat16* src = (mv.value ? a.xv + mv.t * a.xv_sn : a.xk + mv.t * a.xk_sn) + mv.h0 * sh + col;
   uint4 x[kKvUnroll];
 #pragma unroll
   for (int u = 0; u < kKvUnroll; ++u) {
-    const int r = r0 + u * RPW;
     x[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < 2 * a.Hkv) {
-      const __nv_bfloat16* src = r < a.Hkv ? a.xk + t * a.xk_sn + r * a.xk_sh
-                                           : a.xv + t * a.xv_sn + (r - a.Hkv) * a.xv_sh;
-      x[u] = __ldg(reinterpret_cast<const uint4*>(src + col));
-    }
+    if (mv.h0 + u * RPW < a.Hkv) x[u] = __ldg(reinterpret_cast<const uint4*>(src + u * RPW * sh));
   }
-  int b = t, first = t, end = t + 1;
-  if (a.cu) {
-    b = kv_find_seq(a.cu, a.B, t, lane);
-    first = __ldg(a.cu + b);
-    end = __ldg(a.cu + b + 1);
-  }
-  if (t < first || t >= end) return;  // a row of no sequence
-  const long long row = kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
+  bool in_sequence;
+  const int row = kv_place_token(a, mv.t, lane, &in_sequence);
   if (row < 0) return;
   // the largest |x| of each row as bf16 bits -- as integers infinities and NaN sort above all numbers --, two rows to
   // a word on their way through the shuffles
@@ -261,9 +294,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
     tiny |= mb[u] < kTinyBits || mb[u + 1] < kTinyBits;
   }
   const bool lifted = __any_sync(0xffffffffu, tiny);
+  const int at0 = row + (mv.h0 << a.page_shift), step = RPW << a.page_shift;
+  uint8_t* dst = (mv.value ? a.v : a.k) + (long long)at0 * D + col;
+  float* dst_scale = (mv.value ? a.vs : a.ks) + at0;
 #pragma unroll
   for (int u = 0; u < kKvUnroll; ++u) {
-    const int r = r0 + u * RPW;
     const float amax = __uint_as_float(mb[u] << 16);
     // top / amax to an ulp or two (the codes ask for no more), and amax / top by one step of Newton's division on
     // the rounded reciprocal of top: the residual fma is exact, so the quotient is correctly rounded.  A row with an
@@ -291,15 +326,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = f2_mul(y[i], inv2);
     const uint32_t c0 = kv_encode4<FMT>(y[0], y[1]), c1 = kv_encode4<FMT>(y[2], y[3]);
-    if (r < 2 * a.Hkv) {
-      const int h = r < a.Hkv ? r : r - a.Hkv;
-      const long long at = row + ((long long)h << a.page_shift);
-      const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
-      (void)lim;
-      if (FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
-        *reinterpret_cast<uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col) = make_uint2(c0, c1);
-        if (lane % LPR == 0) (r < a.Hkv ? a.ks : a.vs)[at] = scale;
-      }
+    if (mv.h0 + u * RPW < a.Hkv &&
+        FA_IN(kSiteKvRow, (long long)at0 + u * step, 1, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err)) {
+      *reinterpret_cast<uint2*>(dst + (long long)u * step * D) = make_uint2(c0, c1);
+      if (lane % LPR == 0) dst_scale[u * step] = scale;
     }
   }
 }
@@ -308,46 +338,35 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31;
-  const int units = (2 * a.Hkv + kv_rows_per_unit<D>() - 1) / kv_rows_per_unit<D>();
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(w / units);
-  if (t >= a.total) return;
-  const int r0 = (int)(w - (long long)t * units) * kv_rows_per_unit<D>() + lane / LPR;
   const int col = (lane % LPR) * 8;
-  int b = t, first = t, end = t + 1;
-  if (a.cu) {
-    b = kv_find_seq(a.cu, a.B, t, lane);
-    first = __ldg(a.cu + b);
-    end = __ldg(a.cu + b + 1);
-  }
-  if (t < first || t >= end) return;  // a row of no sequence: left as it was
-  const long long row = kv_row(a, b, (long long)(a.lens ? __ldg(a.lens + b) : 0) + (t - first), lane == 0);
-  const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
-  (void)lim;
+  const KvMove mv = kv_move<D>(a, lane);
+  if (mv.t < 0) return;
+  bool in_sequence;
+  const int row = kv_place_token(a, mv.t, lane, &in_sequence);
+  if (!in_sequence) return;  // a row of no sequence: left as it was
+  const int at0 = row + (mv.h0 << a.page_shift), step = RPW << a.page_shift;
+  const uint8_t* src = (mv.value ? a.v : a.k) + (long long)at0 * D + col;
+  const float* src_scale = (mv.value ? a.vs : a.ks) + at0;
   uint2 c[kKvUnroll];
   float sc[kKvUnroll];
 #pragma unroll
   for (int u = 0; u < kKvUnroll; ++u) {
-    const int r = r0 + u * RPW;
-    const int h = r < a.Hkv ? r : r - a.Hkv;
-    const long long at = row + ((long long)h << a.page_shift);
     c[u] = make_uint2(0u, 0u);
     sc[u] = 0.f;
-    if (r < 2 * a.Hkv && row >= 0 && FA_IN(kSiteKvRow, at, 1, lim, a.err)) {
-      c[u] = *reinterpret_cast<const uint2*>((r < a.Hkv ? a.k : a.v) + at * D + col);
-      sc[u] = (r < a.Hkv ? a.ks : a.vs)[at];
+    if (row >= 0 && mv.h0 + u * RPW < a.Hkv &&
+        FA_IN(kSiteKvRow, (long long)at0 + u * step, 1, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err)) {
+      c[u] = __ldg(reinterpret_cast<const uint2*>(src + (long long)u * step * D));
+      sc[u] = __ldg(src_scale + u * step);
     }
   }
+  const long long sh = mv.value ? a.xv_sh : a.xk_sh;
+  __nv_bfloat16* dst = (mv.value ? a.xv + mv.t * a.xv_sn : a.xk + mv.t * a.xk_sn) + mv.h0 * sh + col;
 #pragma unroll
   for (int u = 0; u < kKvUnroll; ++u) {
-    const int r = r0 + u * RPW;
-    if (r >= 2 * a.Hkv) continue;
-    float x[4], y[4];
-    kv_decode4<FMT>(c[u].x, x);
-    kv_decode4<FMT>(c[u].y, y);
-    __nv_bfloat16* dst = r < a.Hkv ? a.xk + t * a.xk_sn + r * a.xk_sh : a.xv + t * a.xv_sn + (r - a.Hkv) * a.xv_sh;
-    st_global_v4(dst + col, pack_bf16x2(x[0] * sc[u], x[1] * sc[u]), pack_bf16x2(x[2] * sc[u], x[3] * sc[u]),
-                 pack_bf16x2(y[0] * sc[u], y[1] * sc[u]), pack_bf16x2(y[2] * sc[u], y[3] * sc[u]));
+    if (mv.h0 + u * RPW >= a.Hkv) continue;
+    const uint64_t s2 = f2_pack(sc[u], sc[u]);
+    const uint2 x = kv_decode4<FMT>(c[u].x, s2), y = kv_decode4<FMT>(c[u].y, s2);
+    st_global_v4(dst + u * RPW * sh, x.x, x.y, y.x, y.y);
   }
 }
 
