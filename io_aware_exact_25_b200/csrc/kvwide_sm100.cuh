@@ -13,11 +13,11 @@
 //   then one    producer: codes and scales from the cache's pages to shared
 //               memory by bulk copies, a page (or 128 rows) at a time;
 //               and two that complete the warpgroup
-// CW is 4, or 8 where items have at most 128 rows (one tile, whose softmax is
-// faster than 4 converter warps, about 4900 clocks a key tile: 64 sequences of
-// drafts of 1 to 5 tokens, 6 heads a group, 256 us with 4, 212 with 8; with two
-// tiles the 8 take issue slots from the softmax: a prompt's chunk, 16 heads, 245
-// us with 4, 271 with 8).
+// CW is 4, or 8 where items have at most 128 rows.  Then both row tiles are the
+// same rows and share the keys: tile 0 takes the even key tiles, tile 1 the odd
+// ones, each with its own maximum, sum and O, and tile 0 adds the two up at the
+// end (tile 1's O is in the same tensor-memory lanes).  With 4 converter warps,
+// about 4900 clocks a key tile, the softmax would wait for them.
 // The converter threads take 16 codes at a time, unpack them exactly as the
 // narrow kernel does and write the f16 tile in the 128-byte swizzled layout the
 // MMA reads: 256 rows share one conversion.  (They first loaded the codes
@@ -63,18 +63,21 @@ struct KvWideLayout {
   static_assert(256 * kRegsSoftmax + 32 * CW * kRegsConvert + 128 * kRegsCtl <= kRegsLaunch * kThreads, "register split");
   static constexpr uint32_t kHalf = 128u * 128u;    // 128 rows x 64 f16 columns
   static constexpr uint32_t kTile = 128u * D * 2u;  // 128 x D f16
+  static constexpr bool kSplit = CW == 8;  // at most 128 rows: the two tiles share the keys, and one Q tile is enough
   // K/V operand ring.  Four tiles: K(j + 1) then takes the place of K(j - 1), which the step before freed; with three
   // it took V(j - 1)'s, freed at the end of step j, and its conversion stood in the way (1200 clocks of 4100 a tile).
   static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kRaw = D == 128 ? 2 : 4;  // ring of codes: K(j), V(j), K(j + 1), ...
+  // ring of codes: K(j), V(j), K(j + 1), ...; at d = 128 kSplit has the place of the second Q tile for a third
+  static constexpr int kRaw = D == 128 ? (kSplit ? 3 : 2) : 4;
+  static constexpr int kRawScales = kRaw == 2 ? 1 : 2;  // scales of K(j), V(j), by j
   static constexpr uint32_t kRawCodes = 128u * D;
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffKV = 2 * kTile;
+  static constexpr uint32_t kOffKV = (kSplit ? 1 : 2) * kTile;
   static constexpr uint32_t kOffRaw = kOffKV + kStages * kTile;
-  static constexpr uint32_t kOffRawScale = kOffRaw + kRaw * kRawCodes;  // [kRaw / 2] 128 K scales, 128 V scales
-  static constexpr uint32_t kOffScale = kOffRawScale + kRaw / 2 * 1024;  // [2] 128 K scales times the softmax scale
-  static constexpr uint32_t kOffMisc = kOffScale + 2 * 512;        // [2] {V power, -, -, -, NaN keys [4]}, [2][4] maxima
-  static constexpr uint32_t kOffBar = kOffMisc + 2 * 32 + 2 * 16;
+  static constexpr uint32_t kOffRawScale = kOffRaw + kRaw * kRawCodes;  // [kRawScales] 128 K scales, 128 V scales
+  static constexpr uint32_t kOffScale = kOffRawScale + kRawScales * 1024;  // [2] 128 K scales times the softmax scale
+  static constexpr uint32_t kOffMisc = kOffScale + 2 * 512;  // [2] {V power, -, -, -, keys of non-finite V scale [4]}
+  static constexpr uint32_t kOffBar = kOffMisc + 2 * 32;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kRaw + 2 + 4 + 2 + 2 + 2 + 1 + 1;
   static constexpr uint32_t kOffScan = kOffBar + kNumBars * 8 + 16;
   static constexpr uint32_t kSmem = kOffScan + (uint32_t)sizeof(KvScan);
@@ -142,6 +145,17 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
       : "memory");
 }
 
+// Two columns of a thread's lane.
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld2_sync(uint32_t taddr, uint32_t& a, uint32_t& b) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+  tmem_ld_wait();
+  asm volatile("" : "+r"(a), "+r"(b) : : "memory");
+}
+
 __device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -163,8 +177,8 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
   uint64_t* bar_pv = bar_p + 4;                        // [2] O_t += P_t V done
   uint64_t* bar_sc_full = bar_pv + 2;                  // [2] scales of a key tile written (128)
   uint64_t* bar_sc_empty = bar_sc_full + 2;            // [2] scales consumed (8 warps)
-  uint64_t* bar_vmax = bar_sc_empty + 2;               //     the converter warps' V maxima written
-  uint64_t* bar_drain = bar_vmax + 1;                  //     every MMA retired
+  uint64_t* bar_half = bar_sc_empty + 2;               //     kSplit: tile 1's half of the keys is done (4 warps)
+  uint64_t* bar_drain = bar_half + 1;                  //     every MMA retired
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const uint32_t sbase = smem_u32(smem);
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       mbar_init(&bar_raw_full[i], 1);
       mbar_init(&bar_raw_empty[i], L::kConvertWarps);
     }
-    mbar_init(bar_vmax, L::kConvertWarps);
+    mbar_init(bar_half, 4);
     mbar_init(bar_drain, 1);
     const bool misaligned = (sbase & 1023u) != 0u;
     *abort_flag = misaligned ? 1 : 0;
@@ -242,8 +256,8 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       const uint64_t dk0 = desc_kmajor(sbase + L::kOffKV, 0, L::kHalf);
       const uint64_t dv0 = desc_mnmajor(sbase + L::kOffKV, 0, L::kHalf);
       auto stage_step = [](uint32_t p) { return (uint64_t)((p % L::kStages) * (L::kTile >> 4)); };
-      auto issue_s = [&](int t, uint32_t p) {
-        uint64_t dq = dq0 + (uint64_t)(t * (L::kTile >> 4)), dk = dk0 + stage_step(p);
+      auto issue_s = [&](int t, int tq, uint32_t p) {  // S_t = Q_tq K^T
+        uint64_t dq = dq0 + (uint64_t)(tq * (L::kTile >> 4)), dk = dk0 + stage_step(p);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           mma_ss_elect(tmem + 128u * t, dq, dk, kIdS, kk > 0 ? 1u : 0u);
@@ -278,21 +292,39 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
         const int nt = act1_of() ? 2 : 1;
 #pragma unroll 1
         for (int t = 0; t < nt && ok; ++t) ok = mbar_wait_warp(&bar_q[t], (t ? nq1++ : nq0++) & 1u, ab);
+        if constexpr (L::kSplit) {
+          // step j: O_t += P_t V(j - 2), S_t(j), t = j mod 2
 #pragma unroll 1
-        for (int j = 0; j <= n && ok; ++j) {
-          // tiles in hand: K(j) at pos + 2 j, V(j - 1) at pos + 2 j - 1
-          const uint32_t pk = pos + 2u * j, pv = pk - 1u;
-          if (j > 0 && !(ok = full(pv))) break;
-          if (j < n && !(ok = full(pk))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int t = 0; t < nt && ok; ++t) {
-            if (j > 0) ok = issue_pv(t, j == 1, pv);
-            if (ok && j < n) issue_s(t, pk);
+          for (int j = 0; j < n + 2 && ok; ++j) {
+            const uint32_t pk = pos + 2u * j, pv = pk - 3u;
+            if (j >= 2 && j - 2 < n) {
+              if (!(ok = full(pv)) || !(ok = issue_pv(j & 1, j < 4, pv))) break;
+              mma_commit_elect(&bar_kv_empty[pv % L::kStages]);
+            }
+            if (j < n) {
+              if (!(ok = full(pk))) break;
+              tc_fence_after();
+              issue_s(j & 1, 0, pk);
+              mma_commit_elect(&bar_kv_empty[pk % L::kStages]);
+            }
           }
-          if (!ok) break;
-          if (j > 0) mma_commit_elect(&bar_kv_empty[pv % L::kStages]);
-          if (j < n) mma_commit_elect(&bar_kv_empty[pk % L::kStages]);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j <= n && ok; ++j) {
+            // tiles in hand: K(j) at pos + 2 j, V(j - 1) at pos + 2 j - 1
+            const uint32_t pk = pos + 2u * j, pv = pk - 1u;
+            if (j > 0 && !(ok = full(pv))) break;
+            if (j < n && !(ok = full(pk))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < nt && ok; ++t) {
+              if (j > 0) ok = issue_pv(t, j == 1, pv);
+              if (ok && j < n) issue_s(t, t, pk);
+            }
+            if (!ok) break;
+            if (j > 0) mma_commit_elect(&bar_kv_empty[pv % L::kStages]);
+            if (j < n) mma_commit_elect(&bar_kv_empty[pk % L::kStages]);
+          }
         }
         pos += 2u * n;
         left -= part.take;
@@ -322,18 +354,21 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           const int key = first + j * kKvUnit + g * lane;
           return j < n && g * lane < 128 && key < item_end ? __ldg(trow + (key >> a.page_shift)) : -1;
         };
+        auto row_of = [&](int j, int page) -> long long {
+          const int key = first + j * kKvUnit + g * lane;
+          return (((long long)page * a.Hkv + at.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+        };
         int page_next = fetch(0);
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
-          const int key = first + j * kKvUnit + g * lane;
-          const bool mine = g * lane < 128 && key < item_end;
           int page = page_next;
           page_next = fetch(j + 1);
-          if (mine && (page < 0 || page >= a.num_pages)) {
+          const bool mine = g * lane < 128 && first + j * kKvUnit + g * lane < item_end;
+          if (mine && (uint32_t)page >= (uint32_t)a.num_pages) {
             if (a.err) atomicCAS(a.err, kDevOk, kDevBadPage);
             page = 0;
           }
-          const long long row = (((long long)page * a.Hkv + at.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+          const long long row = row_of(j, page);
           const bool in = mine && FA_IN(kSiteKvRow, row, g, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err);
           const uint32_t rows = (uint32_t)g * (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
 #pragma unroll 1
@@ -343,7 +378,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             if (lane == 0) mbar_arrive_expect_tx(&bar_raw_full[sl], rows * (uint32_t)(which ? D : D + 8));
             __syncwarp();
             uint8_t* dst = smem + L::kOffRaw + sl * L::kRawCodes;
-            uint8_t* dst_sc = smem + L::kOffRawScale + (sl >> 1) * 1024;
+            uint8_t* dst_sc = smem + L::kOffRawScale + (pos >> 1) % L::kRawScales * 1024;
             if (in) {
               bulk_load(dst + g * lane * D, (which ? a.v : a.k) + row * D, (uint32_t)(g * D), &bar_raw_full[sl]);
               if (which == 0) {
@@ -432,29 +467,25 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
         for (int j = 0; j < n; ++j) {
           const uint32_t sl = pos % L::kRaw;
           if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
-          const uint32_t raw_sc = sbase + L::kOffRawScale + (sl >> 1) * 1024;
+          const uint32_t raw_sc = sbase + L::kOffRawScale + (pos >> 1) % L::kRawScales * 1024;
           const int key0 = first + j * kKvUnit;
           const int key = tid & 127;  // whose scales warps 0-3 publish
           const bool in = key0 + key < item_end;
           const float ks = in ? ld_shared_f(raw_sc + 4 * key) : 0.f;
-          const float vk = in ? ld_shared_f(raw_sc + 512 + 4 * key) : 0.f;
           float vs[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) vs[i] = ld_shared_f(raw_sc + 512 + 4 * (i * RP + r_in));
-          // the largest V scale of the tile: warps 0-3 leave theirs, all read (a bounded wait, so that an aborting CTA
-          // cannot strand a warp at a barrier)
-          const uint32_t red = smisc + 64 + (nsc & 1u) * 16;
-          const uint32_t vb = __float_as_uint(vk) & 0x7fffffffu;
-          const uint32_t vnan = __ballot_sync(0xffffffffu, vb >= 0x7f800000u);
-          const uint32_t wmax = __reduce_max_sync(0xffffffffu, vb >= 0x7f800000u ? 0u : vb);
-          if (lane == 0) {
-            if (cw < 4) st_shared_f(red + 4 * cw, __uint_as_float(wmax));
-            mbar_arrive(bar_vmax);  // all of them, so that none can run a tile ahead of another's wait
+          // the largest V scale of the tile, by every warp for itself: four keys a lane
+          const float4 v4 = ld_shared_f4(raw_sc + 512 + 16 * lane);
+          const float vl[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t vmax = 0u, odd[4];  // odd[i], bit l: key 4 l + i has a scale that is not finite
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t vb = key0 + 4 * lane + i < item_end ? __float_as_uint(vl[i]) & 0x7fffffffu : 0u;
+            odd[i] = __ballot_sync(0xffffffffu, vb >= 0x7f800000u);
+            vmax = max(vmax, vb >= 0x7f800000u ? 0u : vb);
           }
-          if (!(ok = mbar_wait_warp(bar_vmax, nsc & 1u, ab))) break;
-          const float4 m4 = ld_shared_f4(red);  // all positive: as integers they sort alike
-          const uint32_t vmax = max(max(__float_as_uint(m4.x), __float_as_uint(m4.y)),
-                                    max(__float_as_uint(m4.z), __float_as_uint(m4.w)));
+          vmax = __reduce_max_sync(0xffffffffu, vmax);
           if (vmax > __float_as_uint(vpower))
             vpower = __uint_as_float(min((vmax & 0x7f800000u) + 0x00800000u, 0x7e800000u));
           const float vinv = __uint_as_float((254u << 23) - __float_as_uint(vpower));
@@ -469,8 +500,10 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           if (cw < 4) {
             if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
             st_shared_f(sscale + st * 512 + 4 * tid, ks * (a.scale_log2 * kv_code_scale<FMT>()));
-            if (lane == 0) st_shared_f(smisc + st * 32 + 16 + 4 * cw, __uint_as_float(vnan));
-            if (tid == 0) st_shared_f(smisc + st * 32, vpower);
+            if (tid == 0) {
+              st_shared_f(smisc + st * 32, vpower);
+              st_shared_v4(smisc + st * 32 + 16, odd[0], odd[1], odd[2], odd[3]);
+            }
             mbar_arrive(&bar_sc_full[st]);
           }
           ++nsc;
@@ -491,6 +524,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       const uint32_t tS = tmem + lane_off + 128u * t;
       const uint32_t tO = tmem + lane_off + L::kColO + D * t;
       uint32_t ns = 0, nsc = 0;  // score tiles and scale stages so far
+      uint32_t nhalf = 0;        // kSplit: items with a second half so far
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
         const int n_item = kv_item_units<false>(a, s, at.rt);
@@ -498,14 +532,14 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
         const int n = part.n;
         if (n == 0) break;
         const int first = begin + part.start * kKvUnit;
-        if (t == 1 && !act1_of()) {
+        if (!L::kSplit && t == 1 && !act1_of()) {
           // no rows here: only release the scales
           for (int j = 0; j < n && ok; ++j, ++nsc) {
             ok = mbar_wait_warp(&bar_sc_full[nsc & 1u], (nsc >> 1) & 1u, ab);
             if (ok && lane == 0) mbar_arrive(&bar_sc_empty[nsc & 1u]);
           }
         } else {
-          const KvRow x = kv_row_of(a, s, at.h, at.rt, t * 128 + r);
+          const KvRow x = kv_row_of(a, s, at.h, at.rt, L::kSplit ? r : t * 128 + r);
           float up = 1.f;
           {
             // this thread's row of Q as f16, columns in the order the codes unpack
@@ -524,16 +558,18 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             const float amax = __uint_as_float(max(m2 & 0xffffu, m2 >> 16) << 16);
             float down = 1.f;
             if (!(amax == 0.f || (amax >= 0.5f && amax < 32768.f))) kv_q_shift(amax, down, up);
-            const uint32_t row = sbase + L::kOffQ + t * L::kTile + r * 128;
+            if (!L::kSplit || t == 0) {
+              const uint32_t row = sbase + L::kOffQ + t * L::kTile + r * 128;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              st_shared_v4(row + (c >> 3) * L::kHalf + (((c & 7) ^ (r & 7)) << 4),
-                           pack_f16x2(bf16_lo(w[c].x) * down, bf16_lo(w[c].y) * down),
-                           pack_f16x2(bf16_hi(w[c].x) * down, bf16_hi(w[c].y) * down),
-                           pack_f16x2(bf16_lo(w[c].z) * down, bf16_lo(w[c].w) * down),
-                           pack_f16x2(bf16_hi(w[c].z) * down, bf16_hi(w[c].w) * down));
-            fence_proxy_async_smem();
-            mbar_arrive(&bar_q[t]);
+              for (int c = 0; c < D / 8; ++c)
+                st_shared_v4(row + (c >> 3) * L::kHalf + (((c & 7) ^ (r & 7)) << 4),
+                             pack_f16x2(bf16_lo(w[c].x) * down, bf16_lo(w[c].y) * down),
+                             pack_f16x2(bf16_hi(w[c].x) * down, bf16_hi(w[c].y) * down),
+                             pack_f16x2(bf16_lo(w[c].z) * down, bf16_lo(w[c].w) * down),
+                             pack_f16x2(bf16_hi(w[c].z) * down, bf16_hi(w[c].w) * down));
+              fence_proxy_async_smem();
+              mbar_arrive(&bar_q[t]);
+            }
           }
           const bool shifted = __any_sync(0xffffffffu, up != 1.f);
           float m = 0.f, l = 0.f, vpower = 0.f;  // m means nothing while l = 0
@@ -542,6 +578,11 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           for (int j = 0; j < n; ++j) {
             const uint32_t st = nsc & 1u;
             if (!(ok = mbar_wait_warp(&bar_sc_full[st], (nsc >> 1) & 1u, ab))) break;
+            if (L::kSplit && (j & 1) != t) {  // the other tile's keys
+              if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
+              ++nsc;
+              continue;
+            }
             if (!(ok = mbar_wait_warp(&bar_s[t], ns & 1u, ab))) break;
             tc_fence_after();
             const uint32_t sK = sscale + st * 512;
@@ -596,7 +637,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
               if ((nb[0] | nb[1] | nb[2] | nb[3]) != 0u) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int k = lim - 32 * i;
+                  const int k = (lim - i + 3) >> 2;  // of the keys 4 l + i those with l < k are visible
                   spoiled |= (nb[i] & (k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0u;
                 }
               }
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
               l *= alpha;
 #pragma unroll
               for (int c = 0; c < 128; ++c) w[c >> 5][c & 31] = __float_as_uint(__uint_as_float(w[c >> 5][c & 31]) - delta);
-              if (j > 0) {
+              if (j > (L::kSplit ? 1 : 0)) {
                 // O_t holds the sum over the earlier tiles (their products completed before S_t(j)), and none is
                 // added before P is published
                 const float f = alpha * vpower * __uint_as_float((254u << 23) - __float_as_uint(vp));
@@ -665,25 +706,57 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             ++ns;
             ++nsc;
           }
-          if (ok) ok = mbar_wait_warp(&bar_pv[t], (ns - 1) & 1u, ab);
-          if (ok) {
+          const bool mine = !L::kSplit || t == 0 || n > 1;  // (a single key tile is all tile 0's)
+          if (ok && mine) ok = mbar_wait_warp(&bar_pv[t], (ns - 1) & 1u, ab);
+          if (ok && mine) {
             tc_fence_after();
             const bool whole = n == n_item;
             if (part.start == 0 && threadIdx.x == 0)
               kv_record(a, *s_line, s, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left) - at.from, n_item, whole,
                         left == total);
-            const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + t * 128 + r;
+            const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + (L::kSplit ? 0 : t * 128) + r;
             float f = l == 0.f ? 0.f : vpower * (kv_code_scale<FMT>() / kv_v_shift<FMT>()) / l;
             if (spoiled) f = __uint_as_float(0x7fc00000u);
-            const float lse2 = l == 0.f ? -INFINITY : m - kKvPShift + log2f(l);
+            float lse2 = l == 0.f ? -INFINITY : m - kKvPShift + log2f(l);
+            float f1 = 0.f;
+            if (L::kSplit && n > 1) {
+              // tile 1 leaves its factor and logsumexp in the lanes of its scores, which nothing overwrites before tile
+              // 0 has loaded the next Q
+              if (t == 1) {
+                tmem_st2(tS, __float_as_uint(f), __float_as_uint(lse2));
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_half);
+              } else if ((ok = mbar_wait_warp(bar_half, nhalf & 1u, ab))) {
+                tc_fence_after();
+                uint32_t w0, w1;
+                tmem_ld2_sync(tS + 128u, w0, w1);
+                const float l1 = __uint_as_float(w1), mx = fmaxf(lse2, l1);
+                const float a0 = kv_weight(lse2, mx), a1 = kv_weight(l1, mx), sum = a0 + a1;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                f *= a0 * inv;
+                f1 = __uint_as_float(w0) * (a1 * inv);
+                lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+              }
+              ++nhalf;
+            }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D && ok && (!L::kSplit || t == 0); c += 16) {
               uint32_t o[16];
               tmem_ld16_sync(tO + c, o);
               float v[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k)  // columns 1 and 2 of each four change places
                 v[(k & ~3) | ((k & 1) << 1) | ((k >> 1) & 1)] = __uint_as_float(o[k]) * f;
+              if (L::kSplit && n > 1) {
+                tmem_ld16_sync(tO + D + c, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  float& y = v[(k & ~3) | ((k & 1) << 1) | ((k >> 1) & 1)];
+                  y = fmaf(__uint_as_float(o[k]), f1, y);
+                }
+              }
               if (x.token >= 0) kv_put_row<D, 16>(a, x, whole, piece, 2ll * gridDim.x * 256, c, v, lse2);
             }
             tc_fence_before();
