@@ -14,7 +14,7 @@
 //
 // The products run on mma.sync m16n8k16 in f16, which a 16-row tile fits
 // (tcgen05's smallest tile has 64 rows, and at 16 rows the tensor pipe is a
-// fifth busy).  Codes become f16 in registers without rounding: an int8 code c
+// quarter busy).  Codes become f16 in registers without rounding: an int8 code c
 // is the byte c + 128 placed under the exponent of 1024, minus 1152; an e4m3
 // code's bits shifted under an f16 sign are its value times 2^-8, subnormals
 // included.  No code, not even a NaN pattern in a slot never written, turns
@@ -30,6 +30,12 @@
 // multiplies p before it is rounded to f16, as a ratio to a running power of
 // two above every V scale seen, so that p * ratio <= 2^15 with 11 significant
 // bits down to 2^-14; the row sum takes the unrounded fp32 p.
+//
+// What bounds it: 64 sequences of 512 to 8192 keys, 8 key heads, d = 128, int8:
+// 124 us, 4.4 TB/s.  The same kernel without its arithmetic streams the bytes in
+// about 104 us; with it the SM issues half of the time and its eight warps wait
+// mostly for one another's dependent instructions (twelve warps of two slices
+// each: the same time).
 #pragma once
 
 #include "kvcache_sm100.cuh"
