@@ -1,7 +1,8 @@
 // fa_kvcache.cu -- host side of the quantised key/value cache and of the
 // attention over it (fa_kv_append, fa_kv_read, fa_fwd_kvcache): argument
 // checks, the choice of kernel, tensor maps and launches on the caller's
-// stream.  Allocates nothing and keeps nothing between calls.
+// stream.  Allocates nothing; what it keeps is, per kernel and
+// device, that its shared-memory limit has been raised.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -152,9 +153,11 @@ struct Choice {
 };
 
 Choice choose(long long rows, int d) {
-  // Up to 16 rows one mma.sync tile holds an item and the cache's bytes are what is waited for.  Above, the wide
-  // kernel: a 32-row narrow one spilled and was slower or no faster (24 heads over one key head, 8 sequences of 512
-  // to 8192 keys: 44 us against 32; 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 254 against 266).
+  // Up to 16 rows one mma.sync tile holds an item and the cache's bytes are what is waited for (64 sequences of 512 to
+  // 8192 keys, 4 rows an item: 128 us here, 320 in the wide kernel; one sequence of 65536: 34 against 54).  Above, the
+  // wide kernel: a 32-row narrow one spilled and was slower or no faster (24 heads over one key head, 8 sequences of
+  // 512 to 8192 keys: 44 us, the wide one 28).  With at most 128 rows its two softmax tiles share an item's keys:
+  // 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 202 us, 243 as two tiles of rows of which one is empty.
   if (rows <= 16) return {16, kSms * (d == 128 ? Narrow<128>::kCtasPerSm : Narrow<64>::kCtasPerSm), 2, true};
   return {256, kSms, 3, rows <= 128};
 }

@@ -32,10 +32,10 @@
 // bits down to 2^-14; the row sum takes the unrounded fp32 p.
 //
 // What bounds it: 64 sequences of 512 to 8192 keys, 8 key heads, d = 128, int8:
-// 124 us, 4.4 TB/s.  The same kernel without its arithmetic streams the bytes in
-// about 104 us; with it the SM issues half of the time and its eight warps wait
-// mostly for one another's dependent instructions (twelve warps of two slices
-// each: the same time).
+// 117-124 us, 4.4-4.7 TB/s.  With the products and the softmax left out the call
+// takes 103 us of 128, so the rest of the way to the bytes' own time is arithmetic:
+// the SM issues half of the time and its eight warps wait mostly for their own
+// dependent instructions (twelve warps of two slices each: the same time).
 #pragma once
 
 #include "kvcache_sm100.cuh"
