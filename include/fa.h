@@ -352,8 +352,9 @@ int fa_bwd_recompute_range(const void* q, const void* k, const void* v, const vo
  * with amax = max |x|, rounding half to even, and stands for code * scale.  A
  * row of zeros has scale 0; a row with an infinity or a NaN has a NaN scale, so
  * every value of it reads as NaN, and attention makes NaN of the query rows that
- * see it and of no others.  page_size is 16, 32, 64 or 128; d is 64 or
- * 128; num_pages * num_kv_heads * page_size is below 2^31.
+ * see it and of no others.  Codes written by other means: e4m3's two NaN
+ * patterns mean nothing, a row is marked by its scale.  page_size is 16, 32, 64
+ * or 128; d is 64 or 128; num_pages * num_kv_heads * page_size is below 2^31.
  *
  * block_table: device int32 [B][max_pages], rows table_stride elements apart:
  * position p of sequence b is slot p % page_size of page

@@ -629,6 +629,13 @@ def _rows_usable(t) -> bool:
     return c == 1 and n >= 0 and h >= 0 and (n | h) & 7 == 0 and t.data_ptr() & 15 == 0
 
 
+def _check_written(name, t, shape, c):
+    """A tensor the kernels write: _check_tokens, and rows they can address, since a copy would not reach the caller."""
+    _check_tokens(name, t, shape, c)
+    if t.numel() and not _rows_usable(t):
+        raise ValueError(f"{name} must have unit last stride, other strides of multiples of 8 and 16-byte alignment")
+
+
 _SixInts = ctypes.c_int64 * 6
 
 
@@ -665,11 +672,11 @@ def kv_read(c: KvBuffers, block_table, total_tokens, starts=None, cu_seqlens=Non
     if k is None:
         k = c.bf16.new_empty(shape)
     else:
-        _check_tokens("k", k, shape, c)
+        _check_written("k", k, shape, c)
     if v is None:
         v = c.bf16.new_empty(shape)
     else:
-        _check_tokens("v", v, shape, c)
+        _check_written("v", v, shape, c)
     _kv_rows(load().fa_kv_read, "fa_kv_read", c, k, v, shape[0], block_table, starts, cu_seqlens)
     return k, v
 
@@ -720,7 +727,7 @@ def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None,
     if o is None:
         o = q.new_empty((T, Hq, d))
     else:
-        _check_tokens("o", o, (T, Hq, d), c)
+        _check_written("o", o, (T, Hq, d), c)
     if lse is not None:
         if lse.dtype != torch.float32 or lse.shape != (Hq, T) or lse.device != c.device or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on the cache's device")

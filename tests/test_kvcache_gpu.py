@@ -681,3 +681,29 @@ def test_lengths_out_of_range_are_clamped_and_reported():
     bad[1, 1] = 1 << 20
     flash_attention_kvcache(x.q, x.cache, bad, x.seqlens)
     assert binding.device_error() == 5
+
+
+def test_outputs_whose_rows_the_kernels_cannot_address_are_refused():
+    """A given output is written in place, so nothing can be copied for it: other strides are an error, and a strided
+    one that can be addressed is written where it says."""
+    x = Batch(INT8, 64, 16, 2, 2, q=[1, 1], lens=[20, 32], seed=54)
+    b, dev = x.cache.buffers, "cuda"
+    want, _ = x.run()
+    attend = lambda o: binding.fwd_kvcache(x.q, b, x.table_dev, x.seqlens, 1, cu_seqlens_q=x.cu, o=o)
+    bf16 = dict(dtype=torch.bfloat16, device=dev)
+    apart = torch.zeros((2, 4, 64, 2), **bf16)[..., 0]     # last stride 2
+    turned = torch.zeros((2, 64, 4), **bf16).transpose(1, 2)
+    narrow = torch.zeros((2, 4, 68), **bf16)[..., :64]     # rows 136 bytes apart
+    shifted = torch.zeros(2 * 4 * 64 + 1, **bf16)[1:].view(2, 4, 64)
+    for o in (apart, turned, narrow, shifted):
+        with pytest.raises(ValueError):
+            attend(o)
+        assert (o == 0).all()
+        kv = o[:, :2]
+        for given in (dict(k=kv), dict(v=kv)):
+            with pytest.raises(ValueError):
+                binding.kv_read(b, x.table_dev, 2, cu_seqlens=x.cu, **given)
+    wide = torch.zeros((2, 4, 128), **bf16)
+    attend(wide[..., :64])
+    assert torch.equal(wide[..., :64].reshape(want.shape), want) and (wide[..., 64:] == 0).all()
+    assert binding.device_error() == 0
