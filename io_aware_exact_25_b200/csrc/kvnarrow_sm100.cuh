@@ -26,10 +26,12 @@
 // Scales: q goes into f16 as it is if the row's largest entry is in [2^-1,
 // 2^15), and shifted by a power of two that its scores take back otherwise
 // (entries below 2^-14 lose bits that stay below 2^-24 of the largest).  K's
-// scale multiplies the fp32 score, in the fma that also subtracts the maximum.  V's scale
-// multiplies p before it is rounded to f16, as a ratio to a running power of
-// two above every V scale seen, so that p * ratio <= 2^15 with 11 significant
-// bits down to 2^-14; the row sum takes the unrounded fp32 p.
+// scale multiplies the fp32 score, in the fma that also subtracts the reference M
+// of the row.  V's scale multiplies p = 2^(x - M + 7) before it is rounded to f16:
+// M is the running maximum of x plus the exponent of a power of two above every V
+// scale that the row has seen (kv_v_top), so p vs <= 2^15 with 11 significant bits
+// down to 2^-14.  Keys that the row does not see have no part in M, however large
+// their scales.  The row sum takes the unrounded fp32 p, on the same scale as O.
 //
 // What bounds it: 64 sequences of 512 to 8192 keys, 8 key heads, d = 128, int8:
 // 117-124 us, 4.4-4.7 TB/s.  With the products and the softmax left out the call
@@ -37,6 +39,8 @@
 // the SM issues half of the time and its eight warps wait mostly for their own
 // dependent instructions (twelve warps of two slices each: the same time).
 #pragma once
+
+#include <type_traits>
 
 #include "kvcache_sm100.cuh"
 
@@ -132,16 +136,32 @@ struct KvNarrowLayout {
   static constexpr uint32_t kRowPad = D + 4;                      // floats of a merged row (bank spread)
   static constexpr uint32_t kOffMerge = 4 * kRingPad;             // [4 warps][16 rows] O; apart from the rings, which are
                                                                   // already filling for the next item
-  static constexpr uint32_t kOffMl = kOffMerge + 4 * 16 * kRowPad * 4;  // [4][kM] m, [4][kM] l, [4] V scale
-  static constexpr uint32_t kOffBar = kOffMl + (8 * kM + 4) * 4;
+  static constexpr uint32_t kOffMl = kOffMerge + 4 * 16 * kRowPad * 4;  // [4][kM] M, l and O's factor
+  static constexpr uint32_t kOffBar = kOffMl + 12 * kM * 4;
   static constexpr uint32_t kOffScan = kOffBar + 4 * kStages * 8 + 16;
   static constexpr uint32_t kSmem = kOffScan + (uint32_t)sizeof(KvScan);
   static_assert(kOffBar % 8 == 0, "barrier alignment");
   static_assert(kCtasPerSm * (kSmem + 1024) <= 233472, "shared memory budget");
 };
 
-// P values carry a factor 2^7 against the running maximum m, which is raised only when a score exceeds it by 8.
+// P values carry a factor 2^7 against the running maximum, which is raised only when a score exceeds it by 8.
 constexpr float kKvPShift = 7.f;
+
+// A row's range of V scales: ve is the biased exponent of a power of two above every finite one that it has seen, 2^(ve -
+// 127).  p carries 2^-(ve - 127) as far as that lies within 2^+-32, which leaves fp32 room for p and its sums; what is
+// beyond (`rest`, 1 for scales of ordinary size) multiplies the scale itself.
+constexpr int kKvVeMin = 1;
+
+__device__ __forceinline__ int kv_v_shift(int ve) { return min(max(127 - ve, -32), 32); }
+__device__ __forceinline__ bool kv_v_beyond(int ve) { return (uint32_t)(ve - 95) > 64u; }
+__device__ __forceinline__ float kv_v_rest(int ve) { return __uint_as_float((uint32_t)(254 - ve - kv_v_shift(ve)) << 23); }
+__device__ __forceinline__ float kv_v_unrest(int ve) { return __uint_as_float((uint32_t)(ve + kv_v_shift(ve)) << 23); }
+
+// The largest x of a row of its kind: 15 + the shift of p.
+__device__ __forceinline__ float kv_v_top(int ve) { return 8.f + kKvPShift + (float)kv_v_shift(ve); }
+
+// Exponent of a power of two above the finite scale of magnitude bits v.
+__device__ __forceinline__ int kv_v_exponent(uint32_t v) { return (int)(v >> 23) + 1; }
 
 // A read that stays where it is written (ahead of the copies that are asked for next).
 __device__ __forceinline__ uint2 ldg_u2_here(const void* p) {
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
   const uint32_t sscale = sring + L::kRingCodes;
   float* s_m = reinterpret_cast<float*>(smem + L::kOffMl);
   float* s_l = s_m + 4 * M;
-  float* s_v = s_l + 4 * M;
+  float* s_v = s_l + 4 * M;  // what a row's O in a warp is to be multiplied by
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4 * S; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + L::kOffBar) + i, 1);
@@ -331,10 +351,15 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     shifted = __any_sync(0xffffffffu, shifted);
 
     float o[D / 8][4];
-    float m[2], l[2];  // m means nothing while the row has seen no key (`seen`, bit half)
+    float m[2], l[2];  // m, the reference M, means nothing while the row has seen no key (`seen`, bit half)
     uint32_t seen = 0u;
-    float vscale = 1.1754943508222875e-38f;  // running power of two above every V scale, at least 2^-126
+    int ve[2];         // the row's range of V scales
+    float top[2];      // kv_v_top of it
+    uint32_t vlim = 0u;  // scales from here on (magnitude bits) are above the range of some row of the warp
+    bool beyond = false;  // some row's range is outside 2^+-32
     m[0] = m[1] = 0.f;
+    ve[0] = ve[1] = kKvVeMin;
+    top[0] = top[1] = kv_v_top(kKvVeMin);
     l[0] = l[1] = 0.f;
 #pragma unroll
     for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
@@ -379,26 +404,22 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
           }
       }
 
-      // ---- V scales: the slice's largest decides whether the running power of two must grow
-      float vmine = ld_shared_f(ssv + 4 * lane);
-      uint32_t vb = __float_as_uint(vmine) & 0x7fffffffu;
-      if (key0 + lane >= item_end || vb >= 0x7f800000u) vb = 0u;  // past the keys, or NaN (which its products carry)
+      // ---- V scales: the slice's largest decides whether some row's range may have to grow
+      uint32_t vb = __float_as_uint(ld_shared_f(ssv + 4 * lane)) & 0x7fffffffu;
+      if (key0 + lane >= item_end || vb >= 0x7f800000u) vb = 0u;  // past the keys, or not finite (its products carry that)
       const uint32_t vmax = __reduce_max_sync(0xffffffffu, vb);
-      bool grow = vmax > __float_as_uint(vscale);
-      float vgrown = vscale;
-      if (grow) vgrown = __uint_as_float(min((vmax & 0x7f800000u) + 0x00800000u, 0x7e800000u));
-      const float vinv = __uint_as_float((254u << 23) - __float_as_uint(vgrown));
+      bool raise = vmax >= vlim;
 
-      // ---- x = score * K scale - (m - 7) against the maxima so far, masks
+      // ---- x = score * K scale - (M - 7) against the references so far, masks
       const float sl2 = a.scale_log2 * kv_code_scale<FMT>();
-      float kscale[4][2], vratio[4][2];
+      float kscale[4][2], vs[4][2];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int kk = nt * 8 + kperm(2 * c4 + e);
           kscale[nt][e] = ld_shared_f(ssk + 4 * kk) * sl2;
-          vratio[nt][e] = ld_shared_f(ssv + 4 * kk) * vinv;
+          vs[nt][e] = ld_shared_f(ssv + 4 * kk);
         }
       if (shifted) {
 #pragma unroll
@@ -406,7 +427,6 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= up[e >> 1];
       }
-      bool raise = grow;
       float mx[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -421,13 +441,18 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
               mx[half] = fmaxf(mx[half], x);
             }
           const bool first_seen = !((seen >> half) & 1u) && mx[half] != -INFINITY;
-          raise |= first_seen || mx[half] > 8.f + kKvPShift;
+          raise |= first_seen || mx[half] > top[half];
         }
       if (__any_sync(0xffffffffu, raise)) {
-        // the first visible scores of a row set its maximum, later ones raise it by what they exceed it
-        const float vs = vscale * vinv;  // both powers of two
-        vscale = vgrown;
-        float alpha[2];
+        // the first visible scores of a row set its maximum, later ones raise it by what they exceed it; a larger range
+        // of V scales raises the reference alone
+        float alpha[2];  // of O; l's lacks the change of `rest`
+        beyond = false;
+        if (masked) {  // a row sees the slice's first keys: vb becomes the largest of a lane's key and those before it
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) vb = max(vb, __shfl_up_sync(0xffffffffu, vb, d));
+        }
+        uint32_t ve_min = 255u;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float x = mx[half];
@@ -435,17 +460,29 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
           const uint32_t bit = 1u << half;
           const bool fresh = !(seen & bit) && x != -INFINITY;
-          const float delta = fresh || x > 8.f + kKvPShift ? x - kKvPShift : 0.f;
+          const int nvis = masked ? min(end[half] - key0, 32) : 32;  // keys of the slice that the row sees
+          const uint32_t vseen = masked ? __shfl_sync(0xffffffffu, vb, max(nvis - 1, 0)) : vmax;
+          const int grown = nvis > 0 ? max(ve[half], kv_v_exponent(vseen)) : ve[half];
+          const float top_old = top[half];
+          top[half] = kv_v_top(grown);
+          const float delta = fresh || x > top_old ? x - (top[half] - 8.f) : top_old - top[half];
           alpha[half] = fresh ? 1.f : ex2(-delta);
           if (fresh) seen |= bit;
           m[half] += delta;
           l[half] *= alpha[half];
-          alpha[half] *= vs;
+          alpha[half] *= kv_v_rest(grown) * kv_v_unrest(ve[half]);
+          ve[half] = grown;
+          if (seen & bit) {
+            beyond |= kv_v_beyond(grown);
+            ve_min = min(ve_min, (uint32_t)grown);
+          }
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) acc[nt][half * 2 + e] -= delta;
         }
+        beyond = __any_sync(0xffffffffu, beyond);
+        vlim = __reduce_min_sync(0xffffffffu, ve_min) << 23;
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) {
           o[t][0] *= alpha[0], o[t][1] *= alpha[0];
@@ -453,10 +490,14 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
         }
       }
 
-      // ---- P = 2^x; the row sum takes P, the product takes f16(P * V scale ratio)
+      // ---- P = 2^x; the row sum takes P, the product takes f16(P * V scale)
       uint32_t pa[2][4];
+      auto probabilities = [&](auto with_rest) {
+        constexpr bool kRest = decltype(with_rest)::value;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          float rest = 1.f;
+          if constexpr (kRest) rest = kv_v_rest(ve[half]);
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
             float pv[2];
@@ -464,13 +505,16 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
             for (int e = 0; e < 2; ++e) {
               const float p = ex2(acc[nt][half * 2 + e]);
               l[half] += p;
-              pv[e] = p * vratio[nt][e];
+              pv[e] = p * (kRest ? vs[nt][e] * rest : vs[nt][e]);
               // a hidden key's scale may be anything, a NaN too
               if (masked && key0 + nt * 8 + kperm(2 * c4 + e) >= end[half]) pv[e] = 0.f;
             }
             pa[nt >> 1][(nt & 1) * 2 + half] = pack_f16x2(pv[0], pv[1]);
           }
         }
+      };
+      if (beyond) probabilities(std::true_type{});
+      else probabilities(std::false_type{});
 
       // ---- O += P V: one ldmatrix covers the slice's 32 keys x 16 columns
 #pragma unroll
@@ -502,7 +546,6 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
     const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * M;
     if (part.start == 0 && threadIdx.x == 0)
       kv_record(a, line, s, at, blockIdx.x, line.cut(blockIdx.x) + (total - left) - at.from, n_item, whole, left == total);
-    if (lane == 0) s_v[warp] = vscale * kv_code_scale<FMT>();
     float* mine = reinterpret_cast<float*>(smem + L::kOffMerge) + warp * 16 * L::kRowPad;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -513,6 +556,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
       if (c4 == 0) {
         s_m[warp * M + r] = (seen >> half) & 1u ? m[half] : -INFINITY;
         s_l[warp * M + r] = lr;
+        s_v[warp * M + r] = kv_v_unrest(ve[half]) * kv_code_scale<FMT>();
       }
       // columns 16 ch + 4 c4 + {0, 1, 2, 3}: both n-tiles' columns interleave
 #pragma unroll
@@ -537,7 +581,7 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const float lse2 = sum == 0.f ? -INFINITY : mx - kKvPShift + log2f(sum);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) f[w] *= inv * s_v[w];
+      for (int w = 0; w < 4; ++w) f[w] *= inv * s_v[w * M + r];
       float v[D / 8];
 #pragma unroll
       for (int e = 0; e < D / 8; e += 4) {
