@@ -10,9 +10,10 @@
 //   warps 4-7   softmax of tile 1
 //   then CW     converter: codes to f16 operand tiles
 //   then one    MMA issue (one thread)
-//   then one    producer: codes and scales from the cache's pages to shared
-//               memory by bulk copies, a page (or 128 rows) at a time;
-//               and two that complete the warpgroup
+//   then one    producer: codes from the cache's pages to shared memory by bulk
+//               copies, a page (or 128 rows) at a time
+//   then one    scales, from the pages to what the softmax reads
+//               and one that completes the warpgroup
 // CW is 4, or 8 where items have at most 128 rows.  Then both row tiles are the
 // same rows and share the keys: tile 0 takes the even key tiles, tile 1 the odd
 // ones, each with its own maximum, sum and O, and tile 0 adds the two up at the
@@ -28,20 +29,24 @@
 // at the end.
 //
 // Scales: K's multiply the fp32 scores, in the fma that also subtracts the
-// running maximum; the softmax scale is folded into them.  V's multiply the
-// codes during the conversion, as f16 ratios to a running power of two above
-// every V scale seen (two f16 roundings, 2^-11 each; with the factor
-// kv_v_shift the products stay in f16's normal range down to 2^-22 of the
-// largest scale).  A V scale that is not finite would spoil rows that do not see
-// its key, 0 x NaN: its row enters as zeros, and the rows that see it are made NaN
-// at the end, from a bit set of such keys per tile.  q goes into f16 as it is
-// if the row's largest entry is in [2^-1, 2^15), and shifted by a power of two
-// that its scores take back otherwise.
+// reference M of the row; the softmax scale is folded into them.  V's multiply
+// p = 2^(x - M + 7) before its one rounding to f16, where M is the running maximum of
+// x plus the exponent of a power of two above every V scale that the row has seen,
+// as in the narrow kernel: keys that a row does not see have no part in its result.
+// (Multiplied into V's codes during the conversion, as f16 ratios to one power of
+// two, they cost two more roundings, and a hidden key's large scale the bits of the
+// rows beside it.  The product per score costs the chunk below nothing with int8
+// codes, 245 us a call then and 240 now, and 265 -> 280 with fp8, where the softmax
+// is the longer chain.)  A
+// scale that is not finite makes its products NaN or infinite, of the rows that see
+// its key; for the others p vs is set to 0.  q goes into f16 as it is if the row's
+// largest entry is in [2^-1, 2^15), and shifted by a power of two that its scores
+// take back otherwise.
 //
-// The scores of a row stay in its thread's registers: x = s ks - (m - 7) at
-// once, against the maximum so far, and only where some x exceeds 15 is m
-// raised and x shifted, so the usual tile costs one fma, half a max3, one
-// exponential, half an add and half a conversion per score.
+// The scores of a row stay in its thread's registers: x = s ks - (M - 7) at
+// once, against the reference so far, and only where some x exceeds its row's top
+// is M raised and x shifted, so the usual tile costs one fma, half a max3, one
+// exponential, half an add, half a product and half a conversion per score.
 //
 // What bounds it: a 256-row item takes about 4300 clocks per 128 keys in the
 // steady state (2048 of MMAs; 3200 of one tile's softmax, whose P then waits
@@ -63,10 +68,10 @@ struct KvWideLayout {
   static constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);
   static constexpr int kConvert = 32 * kConvertWarps;
   // launched at 128 registers a thread with 4 converter warps (512 x 128 = 256 x 192 + 128 x 72 + 128 x 56), at 96
-  // with 8 (640 x 96 = 256 x 176 + 256 x 48 + 128 x 32)
+  // with 8 (640 x 96 = 256 x 176 + 256 x 40 + 128 x 48)
   static constexpr uint32_t kRegsLaunch = CW == 4 ? 128 : 96;
-  static constexpr uint32_t kRegsSoftmax = CW == 4 ? 192 : 176, kRegsConvert = CW == 4 ? 72 : 48;
-  static constexpr uint32_t kRegsCtl = CW == 4 ? 56 : 32;
+  static constexpr uint32_t kRegsSoftmax = CW == 4 ? 192 : 176, kRegsConvert = CW == 4 ? 72 : 40;
+  static constexpr uint32_t kRegsCtl = CW == 4 ? 56 : 48;
   static_assert(CW == 4 || CW == 8, "whole warpgroups");
   static_assert(256 * kRegsSoftmax + 32 * CW * kRegsConvert + 128 * kRegsCtl <= kRegsLaunch * kThreads, "register split");
   static constexpr uint32_t kHalf = 128u * 128u;    // 128 rows x 64 f16 columns
@@ -77,15 +82,13 @@ struct KvWideLayout {
   static constexpr int kStages = D == 128 ? 4 : 6;
   // ring of codes: K(j), V(j), K(j + 1), ...; at d = 128 kSplit has the place of the second Q tile for a third
   static constexpr int kRaw = D == 128 ? (kSplit ? 3 : 2) : 4;
-  static constexpr int kRawScales = kRaw == 2 ? 1 : 2;  // scales of K(j), V(j), by j
   static constexpr uint32_t kRawCodes = 128u * D;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = (kSplit ? 1 : 2) * kTile;
   static constexpr uint32_t kOffRaw = kOffKV + kStages * kTile;
-  static constexpr uint32_t kOffRawScale = kOffRaw + kRaw * kRawCodes;  // [kRawScales] 128 K scales, 128 V scales
-  static constexpr uint32_t kOffScale = kOffRawScale + kRawScales * 1024;  // [2] 128 K scales times the softmax scale
-  static constexpr uint32_t kOffMisc = kOffScale + 2 * 512;  // [2] {V power, -, -, -, keys of non-finite V scale [4]}
-  static constexpr uint32_t kOffBar = kOffMisc + 2 * 32;
+  static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawCodes;  // [2] 128 K scales times the softmax scale, 128 V scales
+  static constexpr uint32_t kOffVMax = kOffScale + 2 * 1024;  // [2][32] largest finite |V scale| of the first 4 (i + 1) keys
+  static constexpr uint32_t kOffBar = kOffVMax + 2 * 128;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kRaw + 2 + 4 + 2 + 2 + 2 + 1 + 1;
   static constexpr uint32_t kOffScan = kOffBar + kNumBars * 8 + 16;
   static constexpr uint32_t kSmem = kOffScan + (uint32_t)sizeof(KvScan);
@@ -93,10 +96,6 @@ struct KvWideLayout {
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kOffScan % 8 == 0, "scan scratch alignment");
 };
-
-// V operands carry this power of two above code * ratio: 128 * 2^8 and 448 / 256 * 2^15 stay below f16's largest number.
-template <int FMT>
-__host__ __device__ constexpr float kv_v_shift() { return FMT == kKvInt8 ? 256.f : 32768.f; }
 
 // Instruction descriptor of kind::f16 with f16 inputs and fp32 accumulation (format codes 0; the other fields as
 // idesc_bf16).
@@ -164,8 +163,20 @@ __device__ __forceinline__ void tmem_ld2_sync(uint32_t taddr, uint32_t& a, uint3
   asm volatile("" : "+r"(a), "+r"(b) : : "memory");
 }
 
-__device__ __forceinline__ void st_shared_f(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ uint32_t ld_shared_u(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_shared_u(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Magnitude bits of a scale, 0 if it is not finite.
+__device__ __forceinline__ uint32_t kv_finite_bits(uint32_t v) {
+  v &= 0x7fffffffu;
+  return v < 0x7f800000u ? v : 0u;
 }
 
 template <int D, int FMT, int CW>
@@ -183,14 +194,14 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
   uint64_t* bar_s = bar_raw_empty + L::kRaw;           // [2] S_t ready
   uint64_t* bar_p = bar_s + 2;                         // [2][2] half h of P_t written (128)
   uint64_t* bar_pv = bar_p + 4;                        // [2] O_t += P_t V done
-  uint64_t* bar_sc_full = bar_pv + 2;                  // [2] scales of a key tile written (128)
+  uint64_t* bar_sc_full = bar_pv + 2;                  // [2] scales of a key tile written (32)
   uint64_t* bar_sc_empty = bar_sc_full + 2;            // [2] scales consumed (8 warps)
   uint64_t* bar_half = bar_sc_empty + 2;               //     kSplit: tile 1's half of the keys is done (4 warps)
   uint64_t* bar_drain = bar_half + 1;                  //     every MMA retired
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t sscale = sbase + L::kOffScale, smisc = sbase + L::kOffMisc;
+  const uint32_t sscale = sbase + L::kOffScale, svmax = sbase + L::kOffVMax;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -199,7 +210,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       mbar_init(&bar_p[2 * t], 128);
       mbar_init(&bar_p[2 * t + 1], 128);
       mbar_init(&bar_pv[t], 1);
-      mbar_init(&bar_sc_full[t], 128);
+      mbar_init(&bar_sc_full[t], 32);
       mbar_init(&bar_sc_empty[t], L::kSoftmaxWarps);
     }
     for (int i = 0; i < L::kStages; ++i) {
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       // ------------------------------------------------------- producer
       // Lane l brings rows [l g, (l + 1) g) of a tile, g = min(page size, 128): they are contiguous in their page.
       // Rows past the item's keys are not asked for unless they share a page with a key; what the slot held before
-      // stands in for them (any code is finite, and the converter gives such keys scale 0).
+      // stands in for them (any code is finite, and such keys have scale 0).
       const int g = min(1 << a.page_shift, 128);
       uint32_t pos = 0;
       bool ok = true;
@@ -383,17 +394,10 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           for (int which = 0; which < 2; ++which) {
             const uint32_t sl = pos % L::kRaw;
             if (!(ok = mbar_wait_warp(&bar_raw_empty[sl], ((pos / L::kRaw) & 1u) ^ 1u, ab))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bar_raw_full[sl], rows * (uint32_t)(which ? D : D + 8));
+            if (lane == 0) mbar_arrive_expect_tx(&bar_raw_full[sl], rows * (uint32_t)D);
             __syncwarp();
             uint8_t* dst = smem + L::kOffRaw + sl * L::kRawCodes;
-            uint8_t* dst_sc = smem + L::kOffRawScale + (pos >> 1) % L::kRawScales * 1024;
-            if (in) {
-              bulk_load(dst + g * lane * D, (which ? a.v : a.k) + row * D, (uint32_t)(g * D), &bar_raw_full[sl]);
-              if (which == 0) {
-                bulk_load(dst_sc + 4 * g * lane, a.ks + row, 4u * g, &bar_raw_full[sl]);
-                bulk_load(dst_sc + 512 + 4 * g * lane, a.vs + row, 4u * g, &bar_raw_full[sl]);
-              }
-            }
+            if (in) bulk_load(dst + g * lane * D, (which ? a.v : a.k) + row * D, (uint32_t)(g * D), &bar_raw_full[sl]);
             ++pos;
           }
         }
@@ -404,6 +408,58 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       for (uint32_t p = pos > L::kRaw ? pos - L::kRaw : 0u; p < pos; ++p)
         mbar_wait_drain(&bar_raw_full[p % L::kRaw], (p / L::kRaw) & 1u);
     }
+    if (run && warp == L::kSoftmaxWarps + L::kConvertWarps + 2) {
+      // --------------------------------------------------------- scales
+      // Lane l brings keys 4 l to 4 l + 3 of a tile, which share a page; the page number comes a tile ahead, and the two
+      // stages keep the scales ahead of the softmax.  Keys past the item's, or of a page outside the cache, have scale 0.
+      uint32_t nsc = 0;
+      bool ok = true;
+      for (int left = total; left > 0 && ok;) {
+        const KvPart part = kv_part(a, kv_item_units<false>(a, s, at.rt), at.from, left);
+        const int n = part.n;
+        if (n == 0) break;  // the stretch ends before the item's first unit
+        const int item_end = kv_item_end<false>(a, s, at.rt);
+        const int key_l = begin + part.start * kKvUnit + 4 * lane;  // this lane's first key of the first tile
+        const int* trow = a.table + (a.phase == kKvPrefix ? 0ll : at.b * a.table_stride);
+        auto page_of = [&](int j) -> int {
+          const int key = key_l + j * kKvUnit;
+          return j < n && key < item_end ? __ldg(trow + (key >> a.page_shift)) : -1;
+        };
+        int page = page_of(0);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++nsc) {
+          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
+          const long long row = (((long long)page * a.Hkv + at.h) << a.page_shift) +
+                                ((key_l + j * kKvUnit) & ((1 << a.page_shift) - 1));
+          if ((uint32_t)page < (uint32_t)a.num_pages &&
+              FA_IN(kSiteKvRow, row, 4, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err)) {
+            k4 = __ldg(reinterpret_cast<const float4*>(a.ks + row));
+            v4 = __ldg(reinterpret_cast<const float4*>(a.vs + row));
+          }
+          page = page_of(j + 1);
+          const uint32_t st = nsc & 1u;
+          if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
+          const int keys = item_end - (key_l + j * kKvUnit);  // of the four
+          const float f = a.scale_log2 * kv_code_scale<FMT>();
+          const float ks[4] = {k4.x * f, k4.y * f, k4.z * f, k4.w * f}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t kb[4], vb[4], vmax = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            kb[i] = i < keys ? __float_as_uint(ks[i]) : 0u;
+            vb[i] = i < keys ? __float_as_uint(vs[i]) : 0u;
+            vmax = max(vmax, kv_finite_bits(vb[i]));
+          }
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) vmax = max(vmax, __shfl_up_sync(0xffffffffu, vmax, d));
+          st_shared_v4(sscale + st * 1024 + 16 * lane, kb[0], kb[1], kb[2], kb[3]);
+          st_shared_v4(sscale + st * 1024 + 512 + 16 * lane, vb[0], vb[1], vb[2], vb[3]);
+          st_shared_u(svmax + st * 128 + 4 * lane, vmax);
+          mbar_arrive(&bar_sc_full[st]);
+        }
+        left -= part.take;
+        if (left > 0 && !kv_next<false>(a, s, at)) break;
+      }
+    }
   } else if (warp >= L::kSoftmaxWarps) {
     regs_dec<L::kRegsConvert>();
     if (run) {
@@ -412,7 +468,6 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       constexpr int RP = L::kConvert / CH; // rows the threads cover in one pass
       constexpr int NP = 128 / RP;         // passes of a tile
       const int tid = threadIdx.x - 32 * L::kSoftmaxWarps;
-      const int cw = warp - L::kSoftmaxWarps;
       const int ch = tid % CH, r_in = tid / CH;
       // the chunk's place in its row of the operand tile: 16 f16 columns are two 16-byte chunks of the 64-column half
       // ch / 4.  At d = 128 eight lanes store one row, and those of the upper half write the second one first, so that
@@ -421,24 +476,21 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
       static_assert(RP % 8 == 0, "a thread's rows share their swizzle");
       const uint32_t row_off = (uint32_t)(ch >> 2) * L::kHalf + r_in * 128;
       const uint32_t off0 = row_off + (((c0 + swap) ^ (r_in & 7)) << 4), off1 = row_off + (((c0 + 1 - swap) ^ (r_in & 7)) << 4);
-      uint32_t pos = 0, nsc = 0;
+      uint32_t pos = 0;
       bool ok = true;
       for (int left = total; left > 0 && ok;) {
         const KvPart part = kv_part(a, kv_item_units<false>(a, s, at.rt), at.from, left);
-        const int n = part.n;
-        if (n == 0) break;  // the stretch ends before the item's first unit
-        const int item_end = kv_item_end<false>(a, s, at.rt);
-        const int first = begin + part.start * kKvUnit;
-        float vpower = 1.1754943508222875e-38f;
-        // the next tile of codes, converted; rows' factors if it is V's
-        auto convert = [&](const uint32_t* ratio) -> bool {
+        if (part.n == 0) break;  // the stretch ends before the item's first unit
+        // tiles K, V, K, V, ...
+#pragma unroll 1
+        for (int j = 0; j < 2 * part.n; ++j, ++pos) {
           const uint32_t st = pos % L::kStages, sl = pos % L::kRaw;
           const uint32_t src = sbase + L::kOffRaw + sl * L::kRawCodes + ch * 16;
-          if (ratio && !mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab)) return false;
+          if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
           uint4 raw[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) raw[i] = ld_shared_u4(src + (i * RP + r_in) * D);
-          if (!mbar_wait_warp(&bar_kv_empty[st], ((pos / L::kStages) & 1u) ^ 1u, ab)) return false;
+          if (!(ok = mbar_wait_warp(&bar_kv_empty[st], ((pos / L::kStages) & 1u) ^ 1u, ab))) break;
           const uint32_t tile = sbase + L::kOffKV + st * L::kTile;
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -447,14 +499,6 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             kv_unpack<FMT>(raw[i].y, w[2], w[3]);
             kv_unpack<FMT>(raw[i].z, w[4], w[5]);
             kv_unpack<FMT>(raw[i].w, w[6], w[7]);
-            if (ratio) {
-              const __half2 f = *reinterpret_cast<const __half2*>(&ratio[i]);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), f);
-                w[e] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-            }
             const uint32_t at0 = tile + off0 + i * (RP * 128), at1 = tile + off1 + i * (RP * 128);
             if (swap) {
               st_shared_v4(at0, w[4], w[5], w[6], w[7]);
@@ -468,55 +512,6 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           mbar_arrive(&bar_kv_full[st]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_raw_empty[sl]);
-          ++pos;
-          return true;
-        };
-#pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const uint32_t sl = pos % L::kRaw;
-          if (!(ok = mbar_wait_warp(&bar_raw_full[sl], (pos / L::kRaw) & 1u, ab))) break;
-          const uint32_t raw_sc = sbase + L::kOffRawScale + (pos >> 1) % L::kRawScales * 1024;
-          const int key0 = first + j * kKvUnit;
-          const int key = tid & 127;  // whose scales warps 0-3 publish
-          const bool in = key0 + key < item_end;
-          const float ks = in ? ld_shared_f(raw_sc + 4 * key) : 0.f;
-          float vs[NP];
-#pragma unroll
-          for (int i = 0; i < NP; ++i) vs[i] = ld_shared_f(raw_sc + 512 + 4 * (i * RP + r_in));
-          // the largest V scale of the tile, by every warp for itself: four keys a lane
-          const float4 v4 = ld_shared_f4(raw_sc + 512 + 16 * lane);
-          const float vl[4] = {v4.x, v4.y, v4.z, v4.w};
-          uint32_t vmax = 0u, odd[4];  // odd[i], bit l: key 4 l + i has a scale that is not finite
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t vb = key0 + 4 * lane + i < item_end ? __float_as_uint(vl[i]) & 0x7fffffffu : 0u;
-            odd[i] = __ballot_sync(0xffffffffu, vb >= 0x7f800000u);
-            vmax = max(vmax, vb >= 0x7f800000u ? 0u : vb);
-          }
-          vmax = __reduce_max_sync(0xffffffffu, vmax);
-          if (vmax > __float_as_uint(vpower))
-            vpower = __uint_as_float(min((vmax & 0x7f800000u) + 0x00800000u, 0x7e800000u));
-          const float vinv = __uint_as_float((254u << 23) - __float_as_uint(vpower));
-          uint32_t ratio[NP];
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const bool use = key0 + i * RP + r_in < item_end && (__float_as_uint(vs[i]) & 0x7fffffffu) < 0x7f800000u;
-            const float f = use ? vs[i] * vinv * kv_v_shift<FMT>() : 0.f;
-            ratio[i] = pack_f16x2(f, f);
-          }
-          const uint32_t st = nsc & 1u;
-          if (cw < 4) {
-            if (!(ok = mbar_wait_warp(&bar_sc_empty[st], ((nsc >> 1) & 1u) ^ 1u, ab))) break;
-            st_shared_f(sscale + st * 512 + 4 * tid, ks * (a.scale_log2 * kv_code_scale<FMT>()));
-            if (tid == 0) {
-              st_shared_f(smisc + st * 32, vpower);
-              st_shared_v4(smisc + st * 32 + 16, odd[0], odd[1], odd[2], odd[3]);
-            }
-            mbar_arrive(&bar_sc_full[st]);
-          }
-          ++nsc;
-          if (!(ok = convert(nullptr))) break;
-          if (!(ok = convert(ratio))) break;
         }
         left -= part.take;
         if (left > 0 && !kv_next<false>(a, s, at)) break;
@@ -547,7 +542,8 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             if (ok && lane == 0) mbar_arrive(&bar_sc_empty[nsc & 1u]);
           }
         } else {
-          const KvRow x = kv_row_of(a, s, at.h, at.rt, L::kSplit ? r : t * 128 + r);
+          KvRow x = kv_row_of(a, s, at.h, at.rt, L::kSplit ? r : t * 128 + r);
+          if (x.token < 0) x.end = 0x7fffffff;  // a row that is not there needs no mask: nothing of it is stored
           float up = 1.f;
           {
             // this thread's row of Q as f16, columns in the order the codes unpack
@@ -580,8 +576,10 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             }
           }
           const bool shifted = __any_sync(0xffffffffu, up != 1.f);
-          float m = 0.f, l = 0.f, vpower = 0.f;  // m means nothing while l = 0
-          bool spoiled = false;                  // the row sees a key whose V scale is not finite
+          float m = 0.f, l = 0.f;  // m, the reference M, means nothing while l = 0
+          int ve = kKvVeMin;       // the row's range of V scales
+          float top = kv_v_top(kKvVeMin);
+          bool beyond = false;     // some row's of the warp is outside 2^+-32
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const uint32_t st = nsc & 1u;
@@ -593,10 +591,10 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             }
             if (!(ok = mbar_wait_warp(&bar_s[t], ns & 1u, ab))) break;
             tc_fence_after();
-            const uint32_t sK = sscale + st * 512;
-            const float vp = ld_shared_f(smisc + st * 32);
+            const uint32_t sK = sscale + st * 1024, sV = sK + 512;
             const int lim = x.end - (first + j * kKvUnit);  // of the tile's keys, those below it are visible
-            const float4 nan4 = ld_shared_f4(smisc + st * 32 + 16);
+            const bool masked = __any_sync(0xffffffffu, lim < 128);
+            uint32_t vmax = ld_shared_u(svmax + st * 128 + 124);  // the largest V scale that the row sees in this tile
             uint32_t w[4][32];
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + 32u * c4, w[c4]);
@@ -620,24 +618,16 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
 #pragma unroll
               for (int e = 0; e < 4; ++e) p[e] = __float_as_uint(y[e]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
-            if (__any_sync(0xffffffffu, lim < 128)) {
+            if (masked) {
 #pragma unroll
               for (int c = 0; c < 128; ++c)
                 if (c >= lim) w[c >> 5][c & 31] = 0xff800000u;
-            }
-            {
-              // keys whose V scale is not finite: does the row see one?
-              const uint32_t nb[4] = {__float_as_uint(nan4.x), __float_as_uint(nan4.y), __float_as_uint(nan4.z),
-                                      __float_as_uint(nan4.w)};
-              if ((nb[0] | nb[1] | nb[2] | nb[3]) != 0u) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int k = (lim - i + 3) >> 2;  // of the keys 4 l + i those with l < k are visible
-                  spoiled |= (nb[i] & (k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u)) != 0u;
-                }
+              if (lim < 128) {
+                const int quads = max(lim, 0) >> 2;
+                vmax = quads > 0 ? ld_shared_u(svmax + st * 128 + 4 * (quads - 1)) : 0u;
+                for (int c = 4 * quads; c < lim; ++c) vmax = max(vmax, kv_finite_bits(ld_shared_u(sV + 4 * c)));
               }
+              __syncwarp();
             }
             float mx4[4];
 #pragma unroll
@@ -649,11 +639,14 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
 #pragma unroll
             for (int g = 0; g < 4; ++g) mx4[g] = fmaxf(mx4[g], __uint_as_float(w[g][31]));
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            // the first visible scores of a row set its maximum, later ones raise it by what they exceed it
+            // the first visible scores of a row set its maximum, later ones raise it by what they exceed it; a larger
+            // range of V scales raises the reference alone
             const bool fresh = l == 0.f && mx != -INFINITY;
-            const bool raise = fresh || mx > 8.f + kKvPShift;
-            if (__any_sync(0xffffffffu, raise) || vp != vpower) {
-              const float delta = raise ? mx - kKvPShift : 0.f;
+            const bool raise = fresh || mx > top || kv_v_exponent(vmax) > ve;
+            if (__any_sync(0xffffffffu, raise)) {
+              const int grown = max(ve, kv_v_exponent(vmax));
+              const float top_new = kv_v_top(grown);
+              const float delta = fresh || mx > top ? mx - (top_new - 8.f) : top - top_new;
               const float alpha = fresh ? 1.f : ex2(-delta);
               m += delta;
               l *= alpha;
@@ -662,7 +655,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
               if (j > (L::kSplit ? 1 : 0)) {
                 // O_t holds the sum over the earlier tiles (their products completed before S_t(j)), and none is
                 // added before P is published
-                const float f = alpha * vpower * __uint_as_float((254u << 23) - __float_as_uint(vp));
+                const float f = alpha * (kv_v_rest(grown) * kv_v_unrest(ve));
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
                   uint32_t o[16];
@@ -673,27 +666,55 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
                 }
                 tmem_st_wait();
               }
-              vpower = vp;
+              ve = grown;
+              top = top_new;
+              beyond = __any_sync(0xffffffffu, (l != 0.f || fresh) && kv_v_beyond(ve));
             }
             uint64_t sum2[2] = {0ull, 0ull};
-            // P in f16 pairs, 64 keys at a time: the product starts on the first half
+            // P times V's scales in f16 pairs, 64 keys at a time: the product starts on the first half
+            auto probabilities = [&](auto with_care) {
+              constexpr bool kCare = decltype(with_care)::value;
+              const float rest = kCare ? kv_v_rest(ve) : 1.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < 2; ++h) {
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                uint32_t pk[16];
+                for (int g = 0; g < 2; ++g) {
+                  uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  const float p0 = ex2(__uint_as_float(w[2 * h + g][2 * c])), p1 = ex2(__uint_as_float(w[2 * h + g][2 * c + 1]));
-                  sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
-                  pk[c] = pack_f16x2(p0, p1);
+                  for (int c = 0; c < 16; c += 2) {
+                    const int c0 = 64 * h + 32 * g + 2 * c;
+                    const float4 v4 = ld_shared_f4(sV + 4 * c0);
+                    const uint32_t* y = &w[2 * h + g][2 * c];
+                    const uint64_t p01 = f2_pack(ex2(__uint_as_float(y[0])), ex2(__uint_as_float(y[1])));
+                    const uint64_t p23 = f2_pack(ex2(__uint_as_float(y[2])), ex2(__uint_as_float(y[3])));
+                    sum2[0] = f2_add(sum2[0], p01);
+                    sum2[1] = f2_add(sum2[1], p23);
+                    float q[4];
+                    if constexpr (kCare) {
+                      const float vs[4] = {v4.x, v4.y, v4.z, v4.w};
+                      f2_unpack(p01, q[0], q[1]);
+                      f2_unpack(p23, q[2], q[3]);
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) q[e] = c0 + e < lim ? q[e] * (vs[e] * rest) : 0.f;
+                    } else {
+                      f2_unpack(f2_mul(p01, f2_pack(v4.x, v4.y)), q[0], q[1]);
+                      f2_unpack(f2_mul(p23, f2_pack(v4.z, v4.w)), q[2], q[3]);
+                    }
+                    pk[c] = pack_f16x2(q[0], q[1]);
+                    pk[c + 1] = pack_f16x2(q[2], q[3]);
+                  }
+                  tmem_st16(tS + 32u * h + 16u * g, pk);
                 }
-                tmem_st16(tS + 32u * h + 16u * g, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bar_p[2 * t + h]);
               }
-              tmem_st_wait();
-              tc_fence_before();
-              mbar_arrive(&bar_p[2 * t + h]);
-            }
+            };
+            // (a hidden key's scale may be anything, a NaN too)
+            if (masked || beyond) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
             {
               float s0, s1, s2, s3;
               f2_unpack(sum2[0], s0, s1);
@@ -712,8 +733,7 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
               kv_record(a, *s_line, s, at, blockIdx.x, s_line->cut(blockIdx.x) + (total - left) - at.from, n_item, whole,
                         left == total);
             const long long piece = (2ll * blockIdx.x + (left == total ? 0 : 1)) * 256 + (L::kSplit ? 0 : t * 128) + r;
-            float f = l == 0.f ? 0.f : vpower * (kv_code_scale<FMT>() / kv_v_shift<FMT>()) / l;
-            if (spoiled) f = __uint_as_float(0x7fc00000u);
+            float f = l == 0.f ? 0.f : kv_v_unrest(ve) * kv_code_scale<FMT>() / l;
             float lse2 = l == 0.f ? -INFINITY : m - kKvPShift + log2f(l);
             float f1 = 0.f;
             if (L::kSplit && n > 1) {

@@ -18,7 +18,7 @@ from test_kvcache_gpu import DTYPES, FP8, INT8, Batch
 
 pytestmark = pytest.mark.gpu
 
-GROUPS = [2]  # with four queries 8 rows per key head
+GROUPS = [2, 20, 80]  # with four queries 8, 80 and 320 rows per key head: each of the kernels
 
 
 def check(x, o, lse, causal=True):
@@ -29,23 +29,23 @@ def check(x, o, lse, causal=True):
         i = torch.arange(nq, device="cuda")
         end = (n - nq + 1 + i).clamp(0, n) if causal else torch.full((nq,), n, device="cuda")
         sees = torch.arange(n, device="cuda")[None] < end[:, None]
-        for h in range(x.Hkv * x.g):
-            q, kk, vv = x.q[t:t + nq, h].double(), k[:, h // x.g], v[:, h // x.g]
-            got, got_lse = o[t:t + nq, h].double(), lse[h, t:t + nq].double()
-            s = (q @ kk.t() * scale).masked_fill(~sees, -math.inf)
-            ref_lse = torch.logsumexp(s, 1)
-            p = torch.exp(s - ref_lse[:, None]).masked_fill(~sees, 0)
-            ref, A = p @ vv, p @ vv.abs()
-            X = ((q.abs() @ kk.abs().t()) * scale).masked_fill(~sees, 0).amax(1)
-            Y = (q.abs().amax(1, keepdim=True) * kk.abs().sum(1)[None] * scale).masked_fill(~sees, 0).amax(1)
-            big = s.abs().masked_fill(~sees, 0).amax(1)
-            delta = 4 * (x.d + 16) * 2.0 ** -24 * X + 2.0 ** -24 * Y + 2.0 ** -21 * (1 + big)
-            V = (vv.abs().amax(1)[None] * sees).amax(1)
-            tol = 2.0 ** -8 * ref.abs() + A * (2.0 ** -11 + 2.0 ** -20 + 2 * delta)[:, None] + (n * 2.0 ** -31 * V)[:, None]
-            off = (got - ref).abs()
-            assert got.isfinite().all(), (b, h)
-            assert (off <= tol).all(), (b, h, (off / tol).max().item())
-            assert ((got_lse - ref_lse).abs() <= delta + 2.0 ** -20 * (1 + ref_lse.abs())).all(), (b, h)
+        # [heads, queries, ...]
+        q, got, got_lse = x.q[t:t + nq].double().transpose(0, 1), o[t:t + nq].double().transpose(0, 1), lse[:, t:t + nq].double()
+        kk, vv = (y.transpose(0, 1).repeat_interleave(x.g, 0) for y in (k, v))
+        s = (q @ kk.mT * scale).masked_fill(~sees, -math.inf)
+        ref_lse = torch.logsumexp(s, 2)
+        p = torch.exp(s - ref_lse[..., None]).masked_fill(~sees, 0)
+        ref, A = p @ vv, p @ vv.abs()
+        X = ((q.abs() @ kk.abs().mT) * scale).masked_fill(~sees, 0).amax(2)
+        Y = (q.abs().amax(2, keepdim=True) * kk.abs().sum(2)[:, None] * scale).masked_fill(~sees, 0).amax(2)
+        big = s.abs().masked_fill(~sees, 0).amax(2)
+        delta = 4 * (x.d + 16) * 2.0 ** -24 * X + 2.0 ** -24 * Y + 2.0 ** -21 * (1 + big)
+        V = (vv.abs().amax(2)[:, None] * sees).amax(2)
+        tol = 2.0 ** -8 * ref.abs() + A * (2.0 ** -11 + 2.0 ** -20 + 2 * delta)[..., None] + (n * 2.0 ** -31 * V)[..., None]
+        off = (got - ref).abs()
+        assert got.isfinite().all(), b
+        assert (off <= tol).all(), (b, (off / tol).max().item())
+        assert ((got_lse - ref_lse).abs() <= delta + 2.0 ** -20 * (1 + ref_lse.abs())).all(), b
         t += nq
     assert binding.device_error() == 0
 
@@ -96,10 +96,36 @@ def test_scales_that_grow_along_the_keys(dtype, g):
     """From 2^-100 to 2^100 over the keys, in steps of a slice and of a key, and falling again."""
     for step in (1, 17, 64):
         x = Batch(dtype, 128, 32, 1, g, q=[3], lens=[1300], seed=6)
-        for pos in range(1300):
-            up = -100 + pos // step * (200 * step / 650)
-            scale_value(x, 0, pos, 2.0 ** min(up, 200 - up, 100))
+        up = -100 + torch.div(torch.arange(1300), step, rounding_mode="floor") * (200 * step / 650)
+        up = torch.minimum(torch.minimum(up, 200 - up), torch.tensor(100.0))
+        page, slot = x.table[0][torch.arange(1300) // 32].long().cuda(), torch.arange(1300).cuda() % 32
+        x.cache.v_scale[page, :, slot] *= torch.exp2(up)[:, None].cuda()
         check(x, *x.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [16, 40, 160])
+def test_one_key_is_its_value(dtype, d, g):
+    """A query of one key returns the value, rounded once to f16 on the way: the codes and their scale enter exactly."""
+    x = Batch(dtype, d, 16, 1, g, q=[1] * 96, lens=[1] * 96, seed=7)
+    check(x, *x.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [16, 40, 160])
+def test_a_value_next_to_a_border_of_bf16(dtype, d, g):
+    """Values above the middle of 1 and 1 + 2^-7 by 1.1 to 2 times 2^-11: one rounding to f16 does not carry them to the
+    other side, two or three do."""
+    x = Batch(dtype, d, 16, 1, g, q=[1] * 256, lens=[1] * 256, seed=17)
+    over = torch.linspace(1.1, 2.0, 256, dtype=torch.float64) * 2.0 ** -11
+    for b in range(256):
+        page = x.table[b, 0].item()
+        code = (3 + 2 * b) % 64 + 64 if dtype == INT8 else 1.0 + b % 8 / 8
+        x.cache.v[page, :, 0] = torch.tensor(code, dtype=torch.float32).to(dtype).cuda()
+        x.cache.v_scale[page, :, 0] = float((1 + 2.0 ** -8) * (1 + over[b]) / code)
+    check(x, *x.run())
 
 
 @pytest.mark.parametrize("g", GROUPS)
