@@ -141,12 +141,13 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // reciprocal good to an ulp, two rounded products), so this rounding puts every
 // border case exactly on its border and moves nothing across one: the code that
 // follows is the exact quotient's, half to even, without a division.  The
-// rounding is Veltkamp's splitting, p = (2^4 + 1) y, (y - p) + p, on both halves
+// rounding is Veltkamp's splitting, p = (2^4 + 1) y, p - (p - y), on both halves
 // of a packed pair (integer operations on the bits are fewer, but go to the
-// pipe that bounds the kernel).
+// pipe that bounds the kernel); in this order a zero keeps its sign.
 __device__ __forceinline__ uint64_t kv_snap2(uint64_t y) {
   const uint64_t p = f2_mul(y, f2_pack(17.f, 17.f));
-  return f2_add(f2_fma(p, f2_pack(-1.f, -1.f), y), p);
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  return f2_fma(f2_fma(y, minus, p), minus, p);
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
