@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   constexpr float kTop = FMT == kKvInt8 ? 127.f : 448.f;
   constexpr uint32_t kTinyBits = (127u - 100u) << 7;  // 2^-100 as a bf16
+  constexpr uint32_t kHugeBits = (127u + 126u) << 7;  // 2^126: above it the reciprocal is subnormal, with fewer bits
   static_assert(kKvUnroll % 2 == 0, "rows go through the shuffles in pairs");
   const int lane = threadIdx.x & 31;
   const int col = (lane % LPR) * 8;
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
                                  __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
     mb[u] = max(m2 & 0xffffu, m2 >> 16);
   }
-  bool tiny = false;  // some row's largest is below 2^-100
+  bool scaled = false;  // some row's largest is below 2^-100, or 2^126 and more
 #pragma unroll
   for (int u = 0; u < kKvUnroll; u += 2) {
     uint32_t m2 = mb[u] | (mb[u + 1] << 16);
@@ -292,9 +293,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
     for (int s = 1; s < LPR; s <<= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, s));
     mb[u] = m2 & 0xffffu;
     mb[u + 1] = m2 >> 16;
-    tiny |= mb[u] < kTinyBits || mb[u + 1] < kTinyBits;
+    scaled |= mb[u] - kTinyBits >= kHugeBits - kTinyBits || mb[u + 1] - kTinyBits >= kHugeBits - kTinyBits;
   }
-  const bool lifted = __any_sync(0xffffffffu, tiny);
+  scaled = __any_sync(0xffffffffu, scaled);
   const int at0 = row + (mv.h0 << a.page_shift), step = RPW << a.page_shift;
   uint8_t* dst = (mv.value ? a.v : a.k) + (long long)at0 * D + col;
   float* dst_scale = (mv.value ? a.vs : a.ks) + at0;
@@ -312,14 +313,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvArgs a) {
     uint64_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = f2_pack(bf16_lo(xs[i]), bf16_hi(xs[i]));
-    if (lifted) {
-      // rows below 2^-100 go up by 2^100, so that nothing leaves fp32's range; a row of zeros keeps scale 0
-      const bool t = mb[u] < kTinyBits;
-      const float lift = t ? 1.2676506002282294e30f : 1.f;
-      if (t) {
-        inv = mb[u] != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
-        scale = __fdiv_rn(amax, kTop);
-      }
+    if (scaled) {
+      // rows below 2^-100 go up by 2^100 and rows of 2^126 and more down by it, so that nothing leaves fp32's normal
+      // range (of a large row entries do that are far too small for a code); a row of zeros keeps scale 0
+      const bool t = mb[u] < kTinyBits, h = mb[u] >= kHugeBits;
+      const float lift = t ? 1.2676506002282294e30f : h ? 7.888609052210118e-31f : 1.f;
+      if (t || h) inv = mb[u] != 0u ? __fdiv_rn(kTop, amax * lift) : 0.f;
+      if (t) scale = __fdiv_rn(amax, kTop);
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = f2_pack(bf16_lo(xs[i]) * lift, bf16_hi(xs[i]) * lift);
     }
