@@ -117,8 +117,14 @@ __device__ __forceinline__ void kv_unpack(uint32_t w, uint32_t& even, uint32_t& 
 template <int FMT>
 __host__ __device__ constexpr float kv_code_scale() { return FMT == kKvInt8 ? 1.f : 256.f; }
 
-// Which power of two scales a row of q into f16: the factor 2^-e and its inverse, from the row's largest |q|.
+// Which power of two scales a row of q into f16: the factor 2^-e and its inverse, from the row's largest |q|.  A row with an
+// infinity or a NaN becomes NaN: its scores are infinities or NaN, and so is their softmax.
 __device__ __forceinline__ void kv_q_shift(float amax, float& down, float& up) {
+  if (__float_as_uint(amax) >= 0x7f800000u) {
+    down = __uint_as_float(0x7fc00000u);
+    up = 1.f;
+    return;
+  }
   const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
   down = __uint_as_float((254u - e) << 23);
   up = __uint_as_float(e << 23);
@@ -422,10 +428,15 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
           vs[nt][e] = ld_shared_f(ssv + 4 * kk);
         }
       if (shifted) {
+        // (K's scale takes the shift first: a large query's keys may be as small as it is large)
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] *= up[e >> 1];
+          for (int e = 0; e < 2; ++e) {
+            acc[nt][e] *= kscale[nt][e] * up[0];
+            acc[nt][2 + e] *= kscale[nt][e] * up[1];
+            kscale[nt][e] = 1.f;
+          }
       }
       float mx[2];
 #pragma unroll

@@ -601,23 +601,25 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             tmem_ld_wait();
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) reg_fence(w[c4]);
-            if (shifted) {
-#pragma unroll
-              for (int c = 0; c < 128; ++c) w[c >> 5][c & 31] = __float_as_uint(__uint_as_float(w[c >> 5][c & 31]) * up);
-            }
             const uint64_t sub2 = f2_pack(kKvPShift - m, kKvPShift - m);
+            auto scores = [&](auto with_shift) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              const float4 k4 = ld_shared_f4(sK + 4 * c);
-              uint32_t* p = &w[c >> 5][c & 31];
-              float y[4];
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1])), f2_pack(k4.x, k4.y), sub2), y[0],
-                        y[1]);
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3])), f2_pack(k4.z, k4.w), sub2), y[2],
-                        y[3]);
+              for (int c = 0; c < 128; c += 4) {
+                float4 k4 = ld_shared_f4(sK + 4 * c);
+                // (K's scale takes the shift: a large query's keys may be as small as it is large)
+                if constexpr (decltype(with_shift)::value) k4.x *= up, k4.y *= up, k4.z *= up, k4.w *= up;
+                uint32_t* p = &w[c >> 5][c & 31];
+                float y[4];
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1])), f2_pack(k4.x, k4.y), sub2), y[0],
+                          y[1]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3])), f2_pack(k4.z, k4.w), sub2), y[2],
+                          y[3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) p[e] = __float_as_uint(y[e]);
-            }
+                for (int e = 0; e < 4; ++e) p[e] = __float_as_uint(y[e]);
+              }
+            };
+            if (shifted) scores(std::true_type{});
+            else scores(std::false_type{});
             if (masked) {
 #pragma unroll
               for (int c = 0; c < 128; ++c)
