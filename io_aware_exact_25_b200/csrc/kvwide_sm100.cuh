@@ -35,13 +35,13 @@
 // as in the narrow kernel: keys that a row does not see have no part in its result.
 // (Multiplied into V's codes during the conversion, as f16 ratios to one power of
 // two, they cost two more roundings, and a hidden key's large scale the bits of the
-// rows beside it.  The product per score costs the chunk below nothing with int8
-// codes, 245 us a call then and 240 now, and 265 -> 280 with fp8, where the softmax
-// is the longer chain.)  A
-// scale that is not finite makes its products NaN or infinite, of the rows that see
-// its key; for the others p vs is set to 0.  q goes into f16 as it is if the row's
-// largest entry is in [2^-1, 2^15), and shifted by a power of two that its scores
-// take back otherwise.
+// rows beside it.  The chunk below took 245 us a call then and 224 now, 269 and
+// 235 with fp8 codes.)  A scale that is not finite makes its products NaN or
+// infinite, of the rows that see its key; only where a tile has one are p vs set to 0
+// for the other rows, in a second form of the loop that is kept off the usual path:
+// taken by every masked tile, the two forms in turn cost the chunk 14 us.  q goes into f16 as
+// it is if the row's largest entry is in [2^-1, 2^15), and shifted by a power of two
+// that its scores take back otherwise.
 //
 // The scores of a row stay in its thread's registers: x = s ks - (M - 7) at
 // once, against the reference so far, and only where some x exceeds its row's top
@@ -87,7 +87,8 @@ struct KvWideLayout {
   static constexpr uint32_t kOffKV = (kSplit ? 1 : 2) * kTile;
   static constexpr uint32_t kOffRaw = kOffKV + kStages * kTile;
   static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawCodes;  // [2] 128 K scales times the softmax scale, 128 V scales
-  static constexpr uint32_t kOffVMax = kOffScale + 2 * 1024;  // [2][32] largest finite |V scale| of the first 4 (i + 1) keys
+  static constexpr uint32_t kOffVMax = kOffScale + 2 * 1024;  // [2][32] largest finite |V scale| of the first 4 (i + 1) keys;
+                                                              // the sign says that the tile has one that is not finite
   static constexpr uint32_t kOffBar = kOffVMax + 2 * 128;
   static constexpr int kNumBars = 2 + 2 * kStages + 2 * kRaw + 2 + 4 + 2 + 2 + 2 + 1 + 1;
   static constexpr uint32_t kOffScan = kOffBar + kNumBars * 8 + 16;
@@ -443,17 +444,20 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
           const float f = a.scale_log2 * kv_code_scale<FMT>();
           const float ks[4] = {k4.x * f, k4.y * f, k4.z * f, k4.w * f}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
           uint32_t kb[4], vb[4], vmax = 0u;
+          bool odd = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             kb[i] = i < keys ? __float_as_uint(ks[i]) : 0u;
             vb[i] = i < keys ? __float_as_uint(vs[i]) : 0u;
             vmax = max(vmax, kv_finite_bits(vb[i]));
+            odd |= (vb[i] & 0x7fffffffu) >= 0x7f800000u;
           }
+          odd = __any_sync(0xffffffffu, odd);
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) vmax = max(vmax, __shfl_up_sync(0xffffffffu, vmax, d));
           st_shared_v4(sscale + st * 1024 + 16 * lane, kb[0], kb[1], kb[2], kb[3]);
           st_shared_v4(sscale + st * 1024 + 512 + 16 * lane, vb[0], vb[1], vb[2], vb[3]);
-          st_shared_u(svmax + st * 128 + 4 * lane, vmax);
+          st_shared_u(svmax + st * 128 + 4 * lane, odd ? vmax | 0x80000000u : vmax);
           mbar_arrive(&bar_sc_full[st]);
         }
         left -= part.take;
@@ -595,6 +599,8 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
             const int lim = x.end - (first + j * kKvUnit);  // of the tile's keys, those below it are visible
             const bool masked = __any_sync(0xffffffffu, lim < 128);
             uint32_t vmax = ld_shared_u(svmax + st * 128 + 124);  // the largest V scale that the row sees in this tile
+            const bool odd = (int)vmax < 0;
+            vmax &= 0x7fffffffu;
             uint32_t w[4][32];
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + 32u * c4, w[c4]);
@@ -618,15 +624,15 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
                 for (int e = 0; e < 4; ++e) p[e] = __float_as_uint(y[e]);
               }
             };
-            if (shifted) scores(std::true_type{});
-            else scores(std::false_type{});
+            if (__builtin_expect(!shifted, 1)) scores(std::false_type{});
+            else scores(std::true_type{});
             if (masked) {
 #pragma unroll
               for (int c = 0; c < 128; ++c)
                 if (c >= lim) w[c >> 5][c & 31] = 0xff800000u;
               if (lim < 128) {
                 const int quads = max(lim, 0) >> 2;
-                vmax = quads > 0 ? ld_shared_u(svmax + st * 128 + 4 * (quads - 1)) : 0u;
+                vmax = quads > 0 ? ld_shared_u(svmax + st * 128 + 4 * (quads - 1)) & 0x7fffffffu : 0u;
                 for (int c = 4 * quads; c < lim; ++c) vmax = max(vmax, kv_finite_bits(ld_shared_u(sV + 4 * c)));
               }
               __syncwarp();
@@ -712,9 +718,9 @@ __global__ void __launch_bounds__(KvWideLayout<D, CW>::kThreads, 1) kv_wide_kern
                 mbar_arrive(&bar_p[2 * t + h]);
               }
             };
-            // (a hidden key's scale may be anything, a NaN too)
-            if (masked || beyond) probabilities(std::true_type{});
-            else probabilities(std::false_type{});
+            // (a hidden key's p is 0, but its scale may be a NaN or infinite)
+            if (__builtin_expect(!(odd || beyond), 1)) probabilities(std::false_type{});
+            else probabilities(std::true_type{});
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
             {
