@@ -409,12 +409,13 @@ int fa_kv_read(const fa_kv_cache* cache, void* k, void* v, const fa_strides* str
  * [B]).  Of its L queries, query i sees keys j < seqlens[b], and when causal
  * j < seqlens[b] - L + i + 1: the queries are the sequence's last tokens.  A
  * query that sees no key gets o = 0 and lse = -inf; rows of no sequence are
- * left as they were.  o must not overlap the inputs.  A sequence with more than
- * max_q query rows is cut to them (device error 3).  Scores are summed in fp32
- * from exact products of q and the codes; a probability times its value's scale
- * is rounded to f16 once for its products with the value's codes.  A query's
- * result depends on the keys that it sees only, whatever the others hold.
- * Results do not depend on the workspace's contents and are
+ * left as they were (max_q = 0: all of them, nothing is launched).  o must not
+ * overlap the inputs.  A sequence with more than max_q query rows is cut to them
+ * (device error 3).  Scores are summed in fp32 from exact products of q and the
+ * codes; a probability times its value's scale is rounded to f16 once for its
+ * products with the value's codes.  A query's result depends on the keys that it
+ * sees only, whatever the others hold; a query with an infinity or a NaN that
+ * sees a key gets NaN.  Results do not depend on the workspace's contents and are
  * the same from run to run.
  *
  * prefix_len > 0 (a multiple of page_size, at most max_pages * page_size)

@@ -696,7 +696,7 @@ def _kv_rows(fn, what, c, k, v, T, block_table, starts, cu_seqlens):
 
 
 def fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len=0) -> int:
-    return int(load().fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, max_q, prefix_len))
+    return int(load().fa_fwd_kvcache_workspace_size(B, Hq, Hkv, d, total_q, min(max_q, total_q), prefix_len))
 
 
 def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None, causal=True, scale=None, prefix_len=0,
@@ -720,6 +720,9 @@ def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None,
         _check_ints("cu_seqlens_q", cu_seqlens_q, c, B + 1)
     elif B * max_q != T:
         raise ValueError("without cu_seqlens_q every sequence has max_q queries")
+    if max_q < 1 and B and T:
+        raise ValueError("max_q is at least 1 where there are queries")
+    max_q = min(max_q, T)
     if prefix_len and (prefix_len % c.page_size != 0 or not 0 <= prefix_len <= max_pages * c.page_size):
         raise ValueError("prefix_len must be a multiple of the page size within the block table")
     if not _rows_usable(q):

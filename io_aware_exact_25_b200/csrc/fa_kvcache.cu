@@ -354,11 +354,13 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   const int Hkv = cache->num_kv_heads, d = cache->d;
   rc = check_attend(B, Hq, Hkv, d, total_q, max_q, prefix_len);
+  // without offsets max_q has to give total_q, also where it is 0
+  if (rc >= 0 && !cu_seqlens_q && B > 0 && Hq > 0 && total_q > 0 && (long long)B * max_q != total_q)
+    return FA_ERR_INVALID_ARG;
   if (rc != FA_OK) return rc == 1 ? FA_OK : rc;
   if ((rc = check_batch(block_table, max_pages, table_stride, B, total_q)) != FA_OK) return rc;
   if (prefix_len % cache->page_size != 0 || (long long)prefix_len > (long long)max_pages * cache->page_size)
     return FA_ERR_INVALID_ARG;
-  if (!cu_seqlens_q && (long long)B * max_q != total_q) return FA_ERR_INVALID_ARG;
   if (!q || !o || !strides || !seqlens) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) || !aligned(cu_seqlens_q, 4))
     return FA_ERR_ALIGNMENT;

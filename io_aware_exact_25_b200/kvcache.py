@@ -87,7 +87,9 @@ def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_
 
     q: bf16, (batch, new tokens, query heads, head_dim), or token-major (T, query heads, head_dim) with
     ``cu_seqlens_q`` (int32 [B + 1]) and ``max_seqlen_q`` (at least the most queries of a sequence) for a ragged
-    batch; a (batch, query heads, head_dim) q without ``cu_seqlens_q`` is one token per sequence.  The query heads are
+    batch; a (batch, query heads, head_dim) q without ``cu_seqlens_q`` is one token per sequence.  Rows of no sequence,
+    and those of a sequence past ``max_seqlen_q`` (an error in ``binding.device_error()``), are not written: what o and
+    the logsumexp hold there is not defined.  The query heads are
     a multiple of the cache's heads; query head h reads key head h // (query heads / key heads).
     ``seqlens`` (int32 [B]) counts each sequence's keys, the new tokens' own included (append them first).  When
     ``causal``, query i of L sees keys j < seqlens[b] - L + i + 1.  A query that sees no key gets zeros.
