@@ -629,6 +629,12 @@ def _rows_usable(t) -> bool:
     return c == 1 and n >= 0 and h >= 0 and (n | h) & 7 == 0 and t.data_ptr() & 15 == 0
 
 
+def _addressable(t):
+    """t, or a copy of it that the kernels can address.  (``contiguous`` gives t itself where it is dense already, off a
+    16-byte boundary or with odd strides of dimensions of size 1 as it may be.)"""
+    return t if _rows_usable(t) else t.clone(memory_format=torch.contiguous_format)
+
+
 def _check_written(name, t, shape, c):
     """A tensor the kernels write: _check_tokens, and rows they can address, since a copy would not reach the caller."""
     _check_tokens(name, t, shape, c)
@@ -655,10 +661,7 @@ def kv_append(c: KvBuffers, k, v, block_table, starts=None, cu_seqlens=None, str
     T = k.shape[0]
     _check_tokens("k", k, (T, c.num_kv_heads, c.d), c)
     _check_tokens("v", v, (T, c.num_kv_heads, c.d), c)
-    if not _rows_usable(k):
-        k = k.contiguous()
-    if not _rows_usable(v):
-        v = v.contiguous()
+    k, v = _addressable(k), _addressable(v)
     _kv_rows(load().fa_kv_append, "fa_kv_append", c, k, v, T, block_table, starts, cu_seqlens)
 
 
@@ -725,8 +728,7 @@ def fwd_kvcache(q, c: KvBuffers, block_table, seqlens, max_q, cu_seqlens_q=None,
     max_q = min(max_q, T)
     if prefix_len and (prefix_len % c.page_size != 0 or not 0 <= prefix_len <= max_pages * c.page_size):
         raise ValueError("prefix_len must be a multiple of the page size within the block table")
-    if not _rows_usable(q):
-        q = q.contiguous()
+    q = _addressable(q)
     if o is None:
         o = q.new_empty((T, Hq, d))
     else:

@@ -34,3 +34,40 @@ def test_a_generous_bound_changes_nothing(n, prefix):
     o2, lse2 = attend(x, n, prefix_len=prefix)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     x.check(o, lse)
+
+
+def moved(t):
+    """The same values in views that the kernels cannot address: off by one element, and (one token, or one head) with
+    a stride that nothing is reached by."""
+    flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:] = t.flatten()
+    out = [flat[1:].view(t.shape)]
+    room = torch.zeros(t.numel() + 64, dtype=t.dtype, device=t.device)
+    for dim in (0, 1):
+        if t.shape[dim] == 1:
+            stride = list(t.stride())
+            stride[dim] = 13
+            out.append(room.as_strided(t.shape, stride).copy_(t))
+    for v in out:
+        assert torch.equal(v, t) and not binding._rows_usable(v)
+    return out
+
+
+@pytest.mark.parametrize("T,Hkv", [(3, 2), (1, 2), (3, 1), (1, 1)])
+def test_inputs_that_the_kernels_cannot_address_are_copied(T, Hkv):
+    x = Batch(INT8, 64, 16, Hkv, 1, q=[T], lens=[40], seed=3)
+    o, lse = attend(x, T)
+    for q in moved(x.q):
+        o2, lse2 = flash_attention_kvcache(q, x.cache, x.table_dev, x.seqlens, cu_seqlens_q=x.cu, max_seqlen_q=T,
+                                           return_lse=True)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    k, v = (torch.randn((T, Hkv, 64), device="cuda").to(torch.bfloat16) for _ in "kv")
+    want = KVCache(1, Hkv, 64, 16, INT8)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    want.append(k, v, table, cu_seqlens=x.cu)
+    for k2, v2 in zip(moved(k), moved(v)):
+        for given in ((k2, v), (k, v2), (k2, v2)):
+            got = KVCache(1, Hkv, 64, 16, INT8)
+            got.append(*given, table, cu_seqlens=x.cu)
+            assert all(torch.equal(getattr(got, n), getattr(want, n)) for n in ("k", "v", "k_scale", "v_scale"))
+    assert binding.device_error() == 0
