@@ -70,8 +70,10 @@ class KVCache:
         k, v: bf16 [T, num_kv_heads, head_dim].  Without ``cu_seqlens`` there is one token per sequence (T = B); with
         it (int32 [B + 1]) sequence b's tokens are rows cu_seqlens[b] to cu_seqlens[b + 1].  They go to positions
         starts[b], starts[b] + 1, ... (int32 [B]; None: from 0).  Sequences may share pages, but not the slots written
-        here.
+        here.  No gradients: k and v that require one are refused, as q is in attention.
         """
+        if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+            raise ValueError("KVCache.append has no backward: detach k and v or use torch.no_grad()")
         binding.kv_append(self.buffers, k, v, block_table, starts, cu_seqlens, stream)
 
     def read(self, block_table, cu_seqlens, total_tokens: int, starts=None, stream=None):

@@ -71,3 +71,20 @@ def test_inputs_that_the_kernels_cannot_address_are_copied(T, Hkv):
             got.append(*given, table, cu_seqlens=x.cu)
             assert all(torch.equal(getattr(got, n), getattr(want, n)) for n in ("k", "v", "k_scale", "v_scale"))
     assert binding.device_error() == 0
+
+
+def test_keys_and_values_that_want_a_gradient_are_refused():
+    """As queries are: nothing of the cache is differentiated."""
+    cache = KVCache(1, 2, 64, 16, INT8)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    x = torch.ones((1, 2, 64), device="cuda").to(torch.bfloat16)
+    grad = x.clone().requires_grad_()
+    for k, v in ((grad, x), (x, grad), (grad, grad * 2)):
+        with pytest.raises(ValueError, match="no backward"):
+            cache.append(k, v, table)
+        assert (cache.k_scale == 0).all()
+        with torch.no_grad():
+            cache.append(k, v, table)
+        cache.append(k.detach(), v.detach(), table)
+        assert (cache.k_scale[0, :, 0] > 0).all()
+        cache.k_scale.zero_()
