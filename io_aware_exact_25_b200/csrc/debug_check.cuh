@@ -37,9 +37,10 @@ enum DbgSite : int {
   kSiteKvRow = 30,       // quantised cache: row (codes and scale) read or written
   kSiteKvO = 31,         // attention over the cache: O row store
   kSiteKvLse = 32,       // attention over the cache: lse store
-  kSiteKvPart = 33,      // attention over the cache: piece store
-  kSiteKvRes = 34,       // attention over the cache: result row of a phase
+  kSiteKvPart = 33,      // attention over the cache: piece store, piece read by a merge
+  kSiteKvRes = 34,       // attention over the cache: result row of a phase, stored or read by a merge
   kSiteKvQ = 35,         // attention over the cache: Q row read
+  kSiteKvCut = 36,       // attention over the cache: entry of an item written, or read by a merge
 };
 
 #ifdef FA_DEBUG

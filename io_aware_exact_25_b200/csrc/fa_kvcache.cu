@@ -165,6 +165,7 @@ Choice choose(long long rows, int d) {
 // Byte offsets in the workspace: the pieces of one launch and the entries that say where they are.
 struct Pieces {
   size_t o, lse, cuts, end;
+  int num_cuts;
 };
 
 Pieces place_pieces(size_t at, const Choice& c, int d, size_t entries) {
@@ -174,6 +175,7 @@ Pieces place_pieces(size_t at, const Choice& c, int d, size_t entries) {
   p.lse = p.o + rows * d * 4;
   p.cuts = round_up(p.lse + rows * 4, 256);
   p.end = round_up(p.cuts + entries * sizeof(fa::KvCut), 256);
+  p.num_cuts = (int)(entries < 0x7fffffff ? entries : 0x7fffffff);  // for the bounds-checking build
   return p;
 }
 
@@ -406,6 +408,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
     a.part_o = reinterpret_cast<float*>(ws + l.pw.o);
     a.part_lse = reinterpret_cast<float*>(ws + l.pw.lse);
     a.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pw.cuts);
+    a.num_cuts = l.pw.num_cuts;
     if ((rc = launch_phase(cache, a, l.whole, st)) != FA_OK) return rc;
     return launch_merge_cut(a, d, l, st);
   }
@@ -418,6 +421,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   pf.part_o = reinterpret_cast<float*>(ws + l.pp.o);
   pf.part_lse = reinterpret_cast<float*>(ws + l.pp.lse);
   pf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.pp.cuts);
+  pf.num_cuts = l.pp.num_cuts;
   pf.row_o = reinterpret_cast<float*>(ws + l.prefix_o);
   pf.row_lse = reinterpret_cast<float*>(ws + l.prefix_lse);
   sf.phase = fa::kKvSuffix;
@@ -428,6 +432,7 @@ int fa_fwd_kvcache(const void* q, void* o, float* lse, const fa_strides* strides
   sf.part_o = reinterpret_cast<float*>(ws + l.ps.o);
   sf.part_lse = reinterpret_cast<float*>(ws + l.ps.lse);
   sf.cuts = reinterpret_cast<fa::KvCut*>(ws + l.ps.cuts);
+  sf.num_cuts = l.ps.num_cuts;
   sf.row_o = reinterpret_cast<float*>(ws + l.suffix_o);
   sf.row_lse = reinterpret_cast<float*>(ws + l.suffix_lse);
   if ((rc = launch_phase(cache, pf, l.prefix, st)) != FA_OK) return rc;

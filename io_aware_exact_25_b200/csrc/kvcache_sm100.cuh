@@ -58,6 +58,7 @@ struct KvArgs {
   float* row_lse;    // [total * Hq], base 2
   struct KvCut* cuts;  // where the pieces are
   int by_item;
+  int num_cuts;        // entries that cuts has room for
 };
 
 // An item's pieces: `first`, then every second one from `next` on, n in all; n = 1 is a finished item.  The entries go
@@ -640,7 +641,8 @@ __device__ __forceinline__ void kv_record(const KvArgs& a, const KvLine& line, c
   k.h = p.h, k.rt = p.rt;
   k.row0 = s.row0, k.lq = s.lq;
   k.pad = 0;
-  a.cuts[a.by_item ? kv_item_index(a, p.b, p.h, p.rt) : c] = k;
+  const long long at = a.by_item ? kv_item_index(a, p.b, p.h, p.rt) : c;
+  if (FA_IN(kSiteKvCut, at, 1, a.num_cuts, a.err)) a.cuts[at] = k;
 }
 
 // Entries that no item will write, before anything else: a CTA's own, or those of tiles that a sequence shorter than
@@ -649,7 +651,7 @@ template <bool ONE>
 __device__ __forceinline__ void kv_clear_cuts(const KvArgs& a) {
   if (a.phase != kKvWhole) return;  // there every entry that is read has its item
   if (!a.by_item) {
-    if (threadIdx.x == 0) a.cuts[blockIdx.x].n = 0;
+    if (threadIdx.x == 0 && FA_IN(kSiteKvCut, (long long)blockIdx.x, 1, a.num_cuts, a.err)) a.cuts[blockIdx.x].n = 0;
     return;
   }
   if (blockIdx.x != 0) return;
@@ -657,8 +659,10 @@ __device__ __forceinline__ void kv_clear_cuts(const KvArgs& a) {
 #pragma unroll 1
   for (int i = threadIdx.x; i < a.B * a.Hkv; i += blockDim.x) {
     const int b = i / a.Hkv;
-    for (int rt = kv_tiles<ONE>(a, kv_seq(a, b, false)); rt < tiles; ++rt)
-      a.cuts[kv_item_index(a, b, i - b * a.Hkv, rt)].n = 0;
+    for (int rt = kv_tiles<ONE>(a, kv_seq(a, b, false)); rt < tiles; ++rt) {
+      const long long at = kv_item_index(a, b, i - b * a.Hkv, rt);
+      if (FA_IN(kSiteKvCut, at, 1, a.num_cuts, a.err)) a.cuts[at].n = 0;
+    }
   }
 }
 
@@ -724,7 +728,7 @@ __device__ __forceinline__ void kv_put_row(const KvArgs& a, const KvRow& x, bool
   const long long row = whole ? (long long)x.token * a.Hq + x.head : piece;
   const long long lim = whole ? (long long)a.total * a.Hq : pieces;
   (void)lim;
-  if (!FA_IN(kSiteKvPart, row, 1, lim, a.err)) return;
+  if (!FA_IN(whole ? kSiteKvRes : kSiteKvPart, row, 1, lim, a.err)) return;
   float* dst = (whole ? a.row_o : a.part_o) + row * D + col0;
 #pragma unroll
   for (int e = 0; e < NC; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -786,6 +790,11 @@ __device__ __forceinline__ KvPieces kv_pieces(const KvArgs& a, const KvCut& k, i
 __device__ __forceinline__ bool kv_cut_ok(const KvArgs& a, const KvCut& k) {
   if (k.n < 1 || k.n > a.G || k.first < 0 || k.first >= 2 * a.G) return false;
   return k.n == 1 || (k.next >= 0 && (long long)k.next + 2ll * (k.n - 2) < 2ll * a.G);
+}
+
+// The pieces that an entry names lie within the launch's (the bounds-checking build's check of kv_merge_row's reads).
+__device__ __forceinline__ bool kv_pieces_in(const KvArgs& a, const KvPieces& p) {
+  return FA_IN(kSiteKvPart, p.at(0), 1, 2ll * a.G * a.M, a.err) && FA_IN(kSiteKvPart, p.at(p.n - 1), 1, 2ll * a.G * a.M, a.err);
 }
 
 template <int D>
@@ -873,6 +882,7 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
   __shared__ KvMergeSmem<D> sm;
   const int warp = threadIdx.x >> 5;
   pdl_wait();
+  if (!FA_IN(kSiteKvCut, (long long)blockIdx.x, 1, a.num_cuts, a.err)) return;
   const KvCut k = a.cuts[blockIdx.x];
   if (k.n < 2 || !kv_cut_ok(a, k)) return;
   const KvSeq s{k.row0, k.lq, 0};
@@ -884,6 +894,7 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_cut_kernel(const KvA
     if (r >= a.M || x.token < 0) continue;
     KvPieces p = kv_pieces(a, k, r), none = p;
     none.n = 0;
+    if (!kv_pieces_in(a, p)) continue;
     kv_merge_row<D>(a, x, p, none, group, sm);
   }
 }
@@ -909,10 +920,14 @@ __global__ void __launch_bounds__(kKvMergeThreads) kv_merge_prefix_kernel(const 
   const uint32_t tp = rp / (uint32_t)pf.M, ts = rs / (uint32_t)sf.M;
   pdl_wait();
   if (i < 0 || i >= ss.lq) return;  // a row of no sequence
-  const KvCut kp = pf.cuts[kv_item_index(pf, 0, h, (int)tp)], ks = sf.cuts[kv_item_index(sf, b, h, (int)ts)];
+  const long long ip = kv_item_index(pf, 0, h, (int)tp), is = kv_item_index(sf, b, h, (int)ts);
+  if (!FA_IN(kSiteKvCut, ip, 1, pf.num_cuts, pf.err) || !FA_IN(kSiteKvCut, is, 1, sf.num_cuts, sf.err)) return;
+  const KvCut kp = pf.cuts[ip], ks = sf.cuts[is];
   if (!kv_cut_ok(pf, kp) || !kv_cut_ok(sf, ks)) return;
   KvPieces p0 = kv_pieces(pf, kp, (int)(rp - tp * (uint32_t)pf.M));
   KvPieces p1 = kv_pieces(sf, ks, (int)(rs - ts * (uint32_t)sf.M));
+  if (!kv_pieces_in(pf, p0) || !kv_pieces_in(sf, p1)) return;
+  if (!FA_IN(kSiteKvRes, (long long)row, 1, (long long)sf.total * sf.Hq, sf.err)) return;
   if (kp.n == 1) p0.o = pf.row_o, p0.lse = pf.row_lse, p0.first = row;
   if (ks.n == 1) p1.o = sf.row_o, p1.lse = sf.row_lse, p1.first = row;
   kv_merge_row<D>(sf, KvRow{t, head, 0}, p0, p1, group, sm);

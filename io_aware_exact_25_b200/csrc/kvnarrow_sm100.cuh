@@ -269,26 +269,35 @@ __global__ void __launch_bounds__(128, L::kCtasPerSm)
       const long long r0 = (((long long)p0 * a.Hkv + ia.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
       uint8_t* dk = ring + st * 2 * L::kCodes;
       uint8_t* dsc = ring + L::kRingCodes + st * 256;
-      (void)FA_IN(kSiteKvRow, r0, two ? 16 : 32, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err);
+      // (a row that fails its check: the map answers the codes' load, the scales are not asked for)
+      const long long lim = ((long long)a.num_pages * a.Hkv) << a.page_shift;
+      (void)lim;
+      const bool in0 = FA_IN(kSiteKvRow, r0, two ? 16 : 32, lim, a.err);
       if (!two) {
-        mbar_arrive_expect_tx(bar, 2 * L::kCodes + 256u);
+        mbar_arrive_expect_tx(bar, 2 * L::kCodes + (in0 ? 256u : 0u));
         tma_load_2d(dk, &tm_k, 0, (int)r0, bar, pol);
         tma_load_2d(dk + L::kCodes, &tm_v, 0, (int)r0, bar, pol);
-        bulk_load(dsc, a.ks + r0, 128, bar);
-        bulk_load(dsc + 128, a.vs + r0, 128, bar);
+        if (in0) {
+          bulk_load(dsc, a.ks + r0, 128, bar);
+          bulk_load(dsc + 128, a.vs + r0, 128, bar);
+        }
       } else {
         // the second page only if the sequence reaches into it: its table entry may not exist
         const bool more = key + 16 < i_end;
-        mbar_arrive_expect_tx(bar, more ? 2 * L::kCodes + 256u : L::kCodes + 128u);
+        const long long r1 = ((long long)p1 * a.Hkv + ia.h) << 4;
+        const bool in1 = more && FA_IN(kSiteKvRow, r1, 16, lim, a.err);
+        mbar_arrive_expect_tx(bar, (more ? 2 * L::kCodes : L::kCodes) + (in0 ? 128u : 0u) + (in1 ? 128u : 0u));
         tma_load_2d(dk, &tm_k, 0, (int)r0, bar, pol);
         tma_load_2d(dk + L::kCodes, &tm_v, 0, (int)r0, bar, pol);
-        bulk_load(dsc, a.ks + r0, 64, bar);
-        bulk_load(dsc + 128, a.vs + r0, 64, bar);
+        if (in0) {
+          bulk_load(dsc, a.ks + r0, 64, bar);
+          bulk_load(dsc + 128, a.vs + r0, 64, bar);
+        }
         if (more) {
-          const long long r1 = ((long long)p1 * a.Hkv + ia.h) << 4;
-          (void)FA_IN(kSiteKvRow, r1, 16, ((long long)a.num_pages * a.Hkv) << a.page_shift, a.err);
           tma_load_2d(dk + L::kCodes / 2, &tm_k, 0, (int)r1, bar, pol);
           tma_load_2d(dk + L::kCodes + L::kCodes / 2, &tm_v, 0, (int)r1, bar, pol);
+        }
+        if (in1) {
           bulk_load(dsc + 64, a.ks + r1, 64, bar);
           bulk_load(dsc + 192, a.vs + r1, 64, bar);
         }
