@@ -88,3 +88,64 @@ def test_keys_and_values_that_want_a_gradient_are_refused():
         cache.append(k.detach(), v.detach(), table)
         assert (cache.k_scale[0, :, 0] > 0).all()
         cache.k_scale.zero_()
+
+
+SHAPES = [  # each kernel and both phases of a shared prefix
+    dict(d=128, page=16, Hkv=2, g=4, q=[1] * 5, lens=[700, 80, 300, 65, 1500], prefix=64),
+    dict(d=64, page=32, Hkv=2, g=4, q=[1] * 20, lens=[1000 + 7 * i for i in range(20)], prefix=960),
+    dict(d=128, page=64, Hkv=1, g=8, q=[5, 3, 4], lens=[900, 70, 2000]),
+    dict(d=128, page=64, Hkv=2, g=2, q=[200, 33], lens=[900, 1300]),
+]
+
+
+@pytest.mark.parametrize("kw", SHAPES)
+@pytest.mark.parametrize("dtype", [INT8, FP8])
+def test_captured_calls_follow_their_lengths(kw, dtype):
+    """A captured call replayed with other lengths and queries, an eager one and another graph's between its replays."""
+    x = Batch(dtype, seed=71, **kw)
+    full = list(x.lens)
+    graphs = []
+    x.run()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = x.run()
+        graphs.append((g, out))
+    shorter = [max(n - 17 - 5 * i, kw.get("prefix", 0) // 2 + nq) for i, (n, nq) in enumerate(zip(full, x.q_lens))]
+    gen = torch.Generator().manual_seed(3)
+    for i, lens in enumerate((full, shorter, [nq for nq in x.q_lens], full)):
+        x.lens = lens
+        x.seqlens.copy_(torch.tensor(lens, dtype=torch.int32))
+        x.q.copy_(torch.randn(x.q.shape, generator=gen))
+        want, want_lse = x.run()
+        x.check(want, want_lse)
+        for g, (o, lse) in (graphs if i % 2 else graphs[::-1]):
+            o.fill_(7)
+            g.replay()
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert binding.device_error() == 0
+
+
+def test_every_shape_at_once_on_streams_of_its_own():
+    xs = [Batch(dtype, seed=72, **kw) for kw in SHAPES for dtype in (INT8, FP8)]
+    want = [x.run() for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(6):
+        for x, s, out in zip(xs, streams, got):
+            with torch.cuda.stream(s):
+                out.append(x.run())
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        for o, lse in out:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    assert binding.device_error() == 0
+
+
+def test_a_page_that_a_sequence_holds_twice():
+    """Nothing says that a table's pages are different ones."""
+    x = Batch(INT8, 128, 16, 2, 4, q=[2, 1], lens=[100, 50], seed=73)
+    x.table[0, 3], x.table[1, 1] = x.table[0, 1], x.table[0, 2]
+    x.table_dev = x.table.cuda()
+    x.check(*x.run())
