@@ -140,8 +140,8 @@ int make_code_map(CUtensorMap* m, const void* base, const fa_kv_cache* c, int bo
 
 constexpr int kSms = 148;
 
-// Ring depth and CTAs per SM of the narrow kernel.  (Three CTAs of two slices a warp at d = 128, 168 registers a
-// thread: the same time, 143 us for 64 sequences of 512 to 8192 keys and 8 key heads; two of three slices: the same.)
+// Ring depth and CTAs per SM of the narrow kernel: at d = 128 two CTAs of two slices a warp are what shared memory has
+// room for beside the merge buffer.
 template <int D>
 using Narrow = fa::KvNarrowLayout<D, D == 128 ? 2 : 3, D == 128 ? 2 : 3>;
 
@@ -154,10 +154,11 @@ struct Choice {
 
 Choice choose(long long rows, int d) {
   // Up to 16 rows one mma.sync tile holds an item and the cache's bytes are what is waited for (64 sequences of 512 to
-  // 8192 keys, 4 rows an item: 128 us here, 320 in the wide kernel; one sequence of 65536: 34 against 54).  Above, the
-  // wide kernel: a 32-row narrow one spilled and was slower or no faster (24 heads over one key head, 8 sequences of
-  // 512 to 8192 keys: 44 us, the wide one 28).  With at most 128 rows its two softmax tiles share an item's keys:
-  // 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 202 us, 243 as two tiles of rows of which one is empty.
+  // 8192 keys, 4 rows an item, int8: 126 us here, 227 in the wide kernel, 279 there as two tiles of rows; fp8 150 and
+  // 241).  Above, the wide kernel: a 32-row narrow one spilled, and was slower when it was tried.  With at most 128 rows
+  // its two softmax tiles share an item's keys: 64 sequences of drafts of 1 to 5 tokens, 6 heads a group: 149 us, 176 as
+  // two tiles of rows of which one is empty.  The rows are those of the longest sequence: a batch of 63 single tokens
+  // and one chunk of 512 takes 414 us in one call, 141 and 78 as two.
   if (rows <= 16) return {16, kSms * (d == 128 ? Narrow<128>::kCtasPerSm : Narrow<64>::kCtasPerSm), 2, true};
   return {256, kSms, 3, rows <= 128};
 }

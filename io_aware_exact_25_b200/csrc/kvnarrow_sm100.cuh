@@ -34,10 +34,10 @@
 // their scales.  The row sum takes the unrounded fp32 p, on the same scale as O.
 //
 // What bounds it: 64 sequences of 512 to 8192 keys, 8 key heads, d = 128, int8:
-// 117-124 us, 4.4-4.7 TB/s.  With the products and the softmax left out the call
-// takes 103 us of 128, so the rest of the way to the bytes' own time is arithmetic:
-// the SM issues half of the time and its eight warps wait mostly for their own
-// dependent instructions (twelve warps of two slices each: the same time).
+// 122 us, 4.5 TB/s.  With the products and the softmax left out the call takes 103
+// us of 128 (fp8: 110 of 150), so the rest of the way to the bytes' own time is
+// arithmetic: the SM issues half of the time and its eight warps wait mostly for
+// their own dependent instructions.
 #pragma once
 
 #include <type_traits>

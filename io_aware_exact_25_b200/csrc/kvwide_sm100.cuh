@@ -17,8 +17,8 @@
 // CW is 4, or 8 where items have at most 128 rows.  Then both row tiles are the
 // same rows and share the keys: tile 0 takes the even key tiles, tile 1 the odd
 // ones, each with its own maximum, sum and O, and tile 0 adds the two up at the
-// end (tile 1's O is in the same tensor-memory lanes).  With 4 converter warps,
-// about 4900 clocks a key tile, the softmax would wait for them.
+// end (tile 1's O is in the same tensor-memory lanes).  The two together go through
+// the keys in 1.5 us a tile instead of 2.5, hence the 8.
 // The converter threads take 16 codes at a time, unpack them exactly as the
 // narrow kernel does and write the f16 tile in the 128-byte swizzled layout the
 // MMA reads: 256 rows share one conversion.  (They first loaded the codes
@@ -48,13 +48,15 @@
 // is M raised and x shifted, so the usual tile costs one fma, half a max3, one
 // exponential, half an add, half a product and half a conversion per score.
 //
-// What bounds it: a 256-row item takes about 4300 clocks per 128 keys in the
-// steady state (2048 of MMAs; 3200 of one tile's softmax, whose P then waits
-// about 1000 for P V and the next S), and about 12 us to end an item and start
-// the next (epilogue, Q, first S).  Four prompts' chunks of 256 to 2048 tokens
-// over up to 8192 keys, 16 heads, d = 128, int8: 232 us, 560 TFLOP/s of the
-// useful products, tensor pipe 30 %; 32768 shared keys of 64 sequences, 8 key
-// heads of 4 query heads, fp8: 67 us.
+// What bounds it: without masks, one item a CTA, d = 128, 128 keys take 2.5 us at
+// 256 rows (int8; 2.6 with fp8) and 1.5 us at up to 128 rows.  Of the 2.5 the MMAs
+// are 1.04 us (2048 clocks) and the exponentials as much (32768, 16 a clock): S of
+// the next key tile waits for P V of this one, and P for the softmax, so that the two
+// hardly overlap within a row tile.  Launch, Q, the first S, the epilogue and the
+// merge add about 25 us to a call.  Four prompts' chunks of 256 to 2048 tokens over
+// up to 8192 keys, 16 heads, d = 128, int8: 209 us, 620 TFLOP/s of the useful
+// products, tensor pipe 33 %; 32768 shared keys of 64 sequences, 8 key heads of 4
+// query heads, fp8: 62 us.
 #pragma once
 
 #include "kvnarrow_sm100.cuh"
@@ -78,7 +80,7 @@ struct KvWideLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;  // 128 x D f16
   static constexpr bool kSplit = CW == 8;  // at most 128 rows: the two tiles share the keys, and one Q tile is enough
   // K/V operand ring.  Four tiles: K(j + 1) then takes the place of K(j - 1), which the step before freed; with three
-  // it took V(j - 1)'s, freed at the end of step j, and its conversion stood in the way (1200 clocks of 4100 a tile).
+  // it took V(j - 1)'s, freed at the end of step j, and its conversion stood in the way (1200 clocks a tile when tried).
   static constexpr int kStages = D == 128 ? 4 : 6;
   // ring of codes: K(j), V(j), K(j + 1), ...; at d = 128 kSplit has the place of the second Q tile for a third
   static constexpr int kRaw = D == 128 ? (kSplit ? 3 : 2) : 4;

@@ -96,6 +96,9 @@ def flash_attention_kvcache(q, cache: KVCache, block_table, seqlens, cu_seqlens_
     ``seqlens`` (int32 [B]) counts each sequence's keys, the new tokens' own included (append them first).  When
     ``causal``, query i of L sees keys j < seqlens[b] - L + i + 1.  A query that sees no key gets zeros.
 
+    How the work is done follows from the longest sequence's rows, max_seqlen_q * query heads / key heads: a prompt's
+    chunk among sequences of one token is faster as a call of its own beside theirs.
+
     ``prefix_len`` > 0 (a multiple of the page size) says that all sequences begin with the same prefix_len keys, in
     the pages of block_table's first row: they are then read once for the batch.  The result is the same.
 
