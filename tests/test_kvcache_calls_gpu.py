@@ -149,3 +149,34 @@ def test_a_page_that_a_sequence_holds_twice():
     x.table[0, 3], x.table[1, 1] = x.table[0, 1], x.table[0, 2]
     x.table_dev = x.table.cuda()
     x.check(*x.run())
+
+
+@pytest.mark.parametrize("kw", SHAPES)
+def test_a_page_outside_the_cache_spoils_its_sequence_only(kw):
+    """It is reported and not touched (device error 5); the other sequences' results stand."""
+    x = Batch(INT8, seed=74, **kw)
+    o, lse = x.run()
+    b, last = len(x.lens) - 1, (x.lens[-1] - 1) // x.page
+    rows = x.T - x.q_lens[-1]
+    for bad in (x.cache.num_pages, -1, (1 << 31) - 1, -(1 << 31)):
+        table = x.table_dev.clone()
+        table[b, last] = bad
+        o2, lse2 = flash_attention_kvcache(x.q, x.cache, table, x.seqlens, cu_seqlens_q=x.cu, max_seqlen_q=max(x.q_lens),
+                                           prefix_len=x.prefix, return_lse=True)
+        assert binding.device_error() == 5
+        assert torch.equal(o[:rows], o2[:rows]) and torch.equal(lse[:, :rows], lse2[:, :rows])
+
+
+@pytest.mark.parametrize("g", [2, 40])
+@pytest.mark.parametrize("prefix", [0, 32])
+@pytest.mark.parametrize("cu", [[0, 3, 1, 4], [-5, 2, 3, 4], [0, 2, 3, 9], [4, 3, 2, 1], [0, 1 << 30, 3, 4]])
+def test_offsets_out_of_order_are_reported(g, prefix, cu):
+    """Device error 3; what they leave of the tensors is read and written inside them."""
+    x = Batch(FP8, 64, 16, 1, g, q=[2, 1, 1], lens=[40, 70, 33], prefix=prefix, seed=75)
+    room = torch.full((3, 4, g, 64), 5.0, device="cuda").to(torch.bfloat16)
+    lse = torch.full((3, g, 4), 5.0, device="cuda")
+    binding.fwd_kvcache(x.q, x.cache.buffers, x.table_dev, x.seqlens, 2,
+                        cu_seqlens_q=torch.tensor(cu, dtype=torch.int32).cuda(), prefix_len=prefix, o=room[1], lse=lse[1])
+    assert binding.device_error() == 3
+    for t in (room, lse):
+        assert (t[0] == 5).all() and (t[2] == 5).all()
